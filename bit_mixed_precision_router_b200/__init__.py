@@ -19,6 +19,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 FMT_W4G128, FMT_BITPLANE8, FMT_NVFP4 = 0, 1, 2
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype_t
+GATE_NONE, GATE_TOKEN, GATE_FULL = 0, 1, 2
 MAX_EXPERTS, MAX_TOPK = 1024, 32
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE", 3: "MOE_ERR_WORKSPACE",
@@ -41,6 +43,18 @@ class ExpertsT(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int), ("w13", ctypes.c_void_p), ("w13_scale", ctypes.c_void_p),
                 ("w2", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p), ("w13_gscale", ctypes.c_void_p),
                 ("w2_gscale", ctypes.c_void_p)]
+
+
+class BlockNormT(ctypes.Structure):
+    _fields_ = [("y", ctypes.c_void_p), ("pair_to_row", ctypes.c_void_p), ("topk_w", ctypes.c_void_p),
+                ("k", ctypes.c_int64), ("w_post", ctypes.c_void_p), ("gate_mode", ctypes.c_int),
+                ("gate", ctypes.c_void_p), ("gate_sigmoid", ctypes.c_int), ("alpha", ctypes.c_float),
+                ("w_next", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class BlockNormGradsT(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
+                ("dw_post", ctypes.c_void_p), ("dw_next", ctypes.c_void_p)]
 
 
 class CachePlanT(ctypes.Structure):
@@ -88,6 +102,20 @@ _SIGS = {
     "moe_grouped_ffn_w4a4": ([_vp, ctypes.POINTER(RoutingT), ctypes.POINTER(ExpertsT), _vp, _i64, _i64, _i64, _i64,
                               _i64, _vp, _vp, _sz, _vp], ctypes.c_int),
     "moe_combine": ([_vp, ctypes.POINTER(RoutingT), _vp, _i64, _i64, _i64, _vp, _vp], ctypes.c_int),
+    "moe_permute_capacity": ([_vp, _i64, _i64, _i64, _i64, ctypes.POINTER(RoutingT), _vp], ctypes.c_int),
+    "moe_sort_rows": ([_vp, ctypes.c_int, ctypes.POINTER(RoutingT), ctypes.c_int, _i64, _i64, _i64, _vp, _vp],
+                      ctypes.c_int),
+    "moe_sort_rows_bwd": ([_vp, ctypes.c_int, ctypes.POINTER(RoutingT), ctypes.c_int, _vp, _i64, _i64, _i64, _vp, _vp,
+                           _vp], ctypes.c_int),
+    "moe_unsort_rows": ([_vp, ctypes.c_int, ctypes.POINTER(RoutingT), ctypes.c_int, _vp, _i64, _i64, _i64, _vp, _vp],
+                        ctypes.c_int),
+    "moe_unsort_rows_bwd": ([_vp, ctypes.c_int, ctypes.POINTER(RoutingT), ctypes.c_int, _vp, _i64, _i64, _i64, _vp,
+                             _vp, _vp], ctypes.c_int),
+    "moe_route_topk_bwd": ([_vp, ctypes.POINTER(RoutingT), _i64, _i64, _i64, _vp, _vp], ctypes.c_int),
+    "moe_block_norm": ([ctypes.POINTER(BlockNormT), _vp, ctypes.c_int, _i64, _i64, _vp, _vp, _vp], ctypes.c_int),
+    "moe_block_norm_bwd_workspace_bytes": ([_i64, _i64], _sz),
+    "moe_block_norm_bwd": ([ctypes.POINTER(BlockNormT), _vp, _vp, _vp, ctypes.c_int, _i64, _i64,
+                            ctypes.POINTER(BlockNormGradsT), _vp, _sz, _vp], ctypes.c_int),
     "moe_gather_rows": ([_vp, _vp, _i64, _i64, _i64, _vp, _vp], ctypes.c_int),
     "moe_ids_from_counts": ([_vp, _i64, _i64, _vp, _vp], ctypes.c_int),
     "moe_check_device_errors": ([_vp], ctypes.c_int),
@@ -617,6 +645,274 @@ def moe_combine(y_rows: torch.Tensor, routing: Routing, T: int, k: int, residual
     rc = routing.c()
     _call("moe_combine", _p(y_rows), ctypes.byref(rc), _p(residual), T, H, k, _p(out), _stream(stream))
     return out
+
+
+# ---------------------------------------------------------------- sorted by expert and back, with gradients
+def _device_of(*tensors) -> torch.device:
+    """The one CUDA device of the given tensors (None skipped)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return dev
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call_on(device: torch.device, stream, name: str, *args) -> None:
+    """_call with the tensors' device current, on `stream` or that device's current stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream of {stream.device} with tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        _call(name, *args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            _call(name, *args, _stream(stream))
+
+
+def _dtype_code(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{what}: expected bf16, fp16 or fp32, got {t.dtype}")
+    return DTYPES[t.dtype]
+
+
+def _matrix(t: torch.Tensor | None, what: str, dtype=None, rows: int | None = None, cols: int | None = None) -> None:
+    """A 2-d tensor of at least `rows` rows of `cols` elements."""
+    if t is None:
+        return
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected 2 dimensions, got {t.dim()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if (rows is not None and t.shape[0] < rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what}: needs at least {rows} rows of {cols}, has {tuple(t.shape)}")
+
+
+def _pairs(routing: Routing, T: int, k: int, weighted: bool) -> RoutingT:
+    """The arrays of a routing that the row calls read."""
+    if T < 0 or k < 1:
+        raise ValueError("T >= 0 and k >= 1 are needed")
+    _check(routing.pair_to_row, "pair_to_row", torch.int32, T * k)
+    if weighted:
+        _check(routing.topk_w, "topk_w", torch.float32, T * k)
+    return RoutingT(None, _p(routing.topk_w) if weighted else None, None, None, _p(routing.pair_to_row), None)
+
+
+def moe_permute_capacity(ids: torch.Tensor, T: int, k: int, E: int, capacity: int = 0, out: Routing | None = None,
+                         stream=None) -> Routing:
+    """moe_permute with dropped pairs: ids outside 0..E-1, and pairs past the first `capacity` of their
+    expert (0: no limit).  Dropped pairs get pair_to_row -1 and follow the last row in sorted_pair.
+    out.topk_ids and out.topk_w are the caller's (not written); without `out`, topk_ids is `ids`."""
+    _check(ids, "ids", torch.int32, T * k)
+    dev = _device_of(ids)
+    if out is None:
+        P = max(T * k, 1)
+        i32 = [_new(n, torch.int32, dev, stream) for n in (E + 1, P, P, E + 1)]
+        out = Routing(ids, None, *i32)
+    else:
+        _check(out.sorted_pair, "sorted_pair", torch.int32, T * k)
+        _check(out.pair_to_row, "pair_to_row", torch.int32, T * k)
+        _check(out.expert_offsets, "expert_offsets", torch.int32, E + 1)
+        _check(out.expert_list, "expert_list", torch.int32, E + 1)
+        _device_of(ids, out.sorted_pair, out.pair_to_row, out.expert_offsets, out.expert_list)
+    rc = RoutingT(None, None, _p(out.expert_offsets), _p(out.sorted_pair), _p(out.pair_to_row), _p(out.expert_list))
+    _call_on(dev, stream, "moe_permute_capacity", _p(ids), T, k, E, capacity, ctypes.byref(rc))
+    return out
+
+
+def moe_sort_rows(x: torch.Tensor, routing: Routing, k: int, weighted: bool = False, rows: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """rows [T*k][H]: each token's row copied to its pairs' rows (times topk_w if weighted).  Rows that
+    no pair refers to are not written."""
+    _matrix(x, "x")
+    T, H = x.shape
+    code = _dtype_code(x, "x")
+    _matrix(rows, "rows", x.dtype, T * k, H)
+    rc = _pairs(routing, T, k, weighted)
+    dev = _device_of(x, rows, routing.pair_to_row, routing.topk_w if weighted else None)
+    rows = _new((max(T * k, 1), H), x.dtype, dev, stream) if rows is None else rows
+    _call_on(dev, stream, "moe_sort_rows", _p(x), code, ctypes.byref(rc), int(weighted), T, H, k, _p(rows))
+    return rows
+
+
+def moe_sort_rows_bwd(d_rows: torch.Tensor, routing: Routing, T: int, k: int, x: torch.Tensor | None = None,
+                      weighted: bool = False, dx: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                      stream=None):
+    """(dx [T][H], dw fp32 [T*k]) of moe_sort_rows; dw (weighted, with x given) else None."""
+    _matrix(d_rows, "d_rows", None, T * k)
+    H = d_rows.shape[1]
+    return _rows_bwd("moe_sort_rows_bwd", d_rows, routing, T, H, k, x, "x", T, weighted, dx, "dx", T, dw, stream)
+
+
+def moe_unsort_rows(rows: torch.Tensor, routing: Routing, T: int, k: int, weighted: bool = True,
+                    residual: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out [T][H]: each token's rows summed (times topk_w if weighted), plus its residual."""
+    _matrix(rows, "rows", None, T * k)
+    H = rows.shape[1]
+    code = _dtype_code(rows, "rows")
+    _matrix(residual, "residual", rows.dtype, T, H)
+    _matrix(out, "out", rows.dtype, T, H)
+    rc = _pairs(routing, T, k, weighted)
+    dev = _device_of(rows, residual, out, routing.pair_to_row, routing.topk_w if weighted else None)
+    out = _new((T, H), rows.dtype, dev, stream) if out is None else out
+    _call_on(dev, stream, "moe_unsort_rows", _p(rows), code, ctypes.byref(rc), int(weighted), _p(residual), T, H, k,
+             _p(out))
+    return out
+
+
+def moe_unsort_rows_bwd(d_out: torch.Tensor, routing: Routing, k: int, rows: torch.Tensor | None = None,
+                        weighted: bool = True, d_rows: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                        stream=None):
+    """(d_rows [T*k][H], dw fp32 [T*k]) of moe_unsort_rows; dw (weighted, with rows given) else None.
+    Rows that no pair refers to are not written."""
+    _matrix(d_out, "d_out")
+    T, H = d_out.shape
+    return _rows_bwd("moe_unsort_rows_bwd", d_out, routing, T, H, k, rows, "rows", T * k, weighted, d_rows, "d_rows",
+                     T * k, dw, stream)
+
+
+def _rows_bwd(name, a, routing, T, H, k, other, other_name, other_rows, weighted, out, out_name, out_rows, dw, stream):
+    code = _dtype_code(a, "the gradient")
+    if other is not None and not weighted:
+        raise ValueError("an unweighted call has no gradient of the weights")
+    if dw is not None and other is None:
+        raise ValueError(f"dw needs {other_name}")
+    _matrix(other, other_name, a.dtype, other_rows, H)
+    _matrix(out, out_name, a.dtype, out_rows, H)
+    _check(dw, "dw", torch.float32, T * k)
+    rc = _pairs(routing, T, k, weighted)
+    dev = _device_of(a, other, out, dw, routing.pair_to_row, routing.topk_w if weighted else None)
+    out = _new((max(out_rows, 1) if out_name == "d_rows" else T, H), a.dtype, dev, stream) if out is None else out
+    if dw is None and other is not None:
+        dw = _new((T * k,), torch.float32, dev, stream)
+    _call_on(dev, stream, name, _p(a), code, ctypes.byref(rc), int(weighted), _p(other), T, H, k, _p(out), _p(dw))
+    return out, dw
+
+
+def moe_route_topk_bwd(dw: torch.Tensor, routing: Routing, T: int, E: int, k: int, d_logits: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """d_logits fp32 [T][E] from the gradient of the routing weights (softmax over each token's k logits)."""
+    _check(dw, "dw", torch.float32, T * k)
+    _check(routing.topk_ids, "topk_ids", torch.int32, T * k)
+    _check(routing.topk_w, "topk_w", torch.float32, T * k)
+    _matrix(d_logits, "d_logits", torch.float32, T, E)
+    dev = _device_of(dw, routing.topk_ids, routing.topk_w, d_logits)
+    d_logits = _new((T, E), torch.float32, dev, stream) if d_logits is None else d_logits
+    rc = RoutingT(_p(routing.topk_ids), _p(routing.topk_w), None, None, None, None)
+    _call_on(dev, stream, "moe_route_topk_bwd", _p(dw), ctypes.byref(rc), T, E, k, _p(d_logits))
+    return d_logits
+
+
+# ---------------------------------------------------------------- norms before and after a block
+def _norm_step(x, y, routing, k, w_post, gate, gate_sigmoid, alpha, w_next, eps):
+    """The moe_block_norm_t of a step over rows like x [T][H], its buffers checked."""
+    _matrix(x, "x")
+    T, H = x.shape
+    code = _dtype_code(x, "x")
+    for w, what in ((w_post, "w_post"), (w_next, "w_next")):
+        if w is not None and w.dtype != x.dtype:
+            raise TypeError(f"{what}: expected {x.dtype}, got {w.dtype}")
+        if w is not None and tuple(w.shape) != (H,):
+            raise ValueError(f"{what}: expected {H} elements, has {tuple(w.shape)}")
+    if y is None and (w_post is not None or gate is not None or routing is not None):
+        raise ValueError("w_post, gate and routing need y")
+    mode = GATE_NONE
+    if gate is not None:
+        mode = GATE_TOKEN if gate.dim() == 1 else GATE_FULL
+        if mode == GATE_TOKEN:
+            _check(gate, "gate", torch.float32, T)
+        else:
+            _matrix(gate, "gate", x.dtype, T, H)
+    row = w = None
+    if routing is not None:
+        _check(routing.pair_to_row, "pair_to_row", torch.int32, T * k)
+        _check(routing.topk_w, "topk_w", torch.float32, T * k)
+        row, w = routing.pair_to_row, routing.topk_w
+    _matrix(y, "y", x.dtype, T * k if routing is not None else T, H)
+    dev = _device_of(x, y, row, w, w_post, gate, w_next)
+    step = BlockNormT(_p(y), _p(row), _p(w), k, _p(w_post), mode, _p(gate), int(gate_sigmoid), alpha, _p(w_next), eps)
+    return step, code, T, H, dev
+
+
+def moe_block_norm(x: torch.Tensor, y: torch.Tensor | None = None, routing: Routing | None = None, k: int = 0,
+                   w_post: torch.Tensor | None = None, gate: torch.Tensor | None = None, gate_sigmoid: bool = False,
+                   alpha: float = 1.0, w_next: torch.Tensor | None = None, eps: float = 1e-6,
+                   z: torch.Tensor | None = None, h: torch.Tensor | None = None, stream=None):
+    """(z, h): z = x + alpha * gate * norm(y) * w_post, the residual stream behind a block (None without
+    y), and h = norm(z) * w_next, the next block's input (None without w_next).  y: the block's
+    output [T][H], or with `routing` its rows [T*k][H], combined with topk_w (None: weight 1).
+    gate: fp32 [T] or [T][H] like x, through a sigmoid if gate_sigmoid.  z may be x."""
+    step, code, T, H, dev = _norm_step(x, y, routing, k, w_post, gate, gate_sigmoid, alpha, w_next, eps)
+    if (z is not None and y is None) or (h is not None and w_next is None):
+        raise ValueError("z needs y, h needs w_next")
+    _matrix(z, "z", x.dtype, T, H)
+    _matrix(h, "h", x.dtype, T, H)
+    _device_of(x, z, h)
+    if z is None and y is not None:
+        z = _new((T, H), x.dtype, dev, stream)
+    if h is None and w_next is not None:
+        h = _new((T, H), x.dtype, dev, stream)
+    _call_on(dev, stream, "moe_block_norm", ctypes.byref(step), _p(x), code, T, H, _p(z), _p(h))
+    return z, h
+
+
+@dataclass
+class BlockNormGrads:
+    """Gradients of moe_block_norm; None where the step has no such input."""
+    dx: torch.Tensor
+    dy: torch.Tensor | None = None
+    dgate: torch.Tensor | None = None
+    dw_post: torch.Tensor | None = None
+    dw_next: torch.Tensor | None = None
+
+
+def moe_block_norm_bwd_workspace_bytes(T: int, H: int) -> int:
+    return int(load().moe_block_norm_bwd_workspace_bytes(T, H))
+
+
+def moe_block_norm_bwd(z: torch.Tensor, dz: torch.Tensor | None = None, dh: torch.Tensor | None = None,
+                       y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                       gate: torch.Tensor | None = None, gate_sigmoid: bool = False, alpha: float = 1.0,
+                       w_next: torch.Tensor | None = None, eps: float = 1e-6,
+                       workspace: torch.Tensor | None = None, stream=None) -> BlockNormGrads:
+    """Gradients of moe_block_norm from z (as it returned it; x for a step without y), the combined y and
+    the gradients dz, dh of its outputs (None: zero; at least one).  dw_next needs dh."""
+    if dz is None and dh is None:
+        raise ValueError("dz or dh is needed")
+    if dh is not None and w_next is None:
+        raise ValueError("dh needs w_next")
+    step, code, T, H, dev = _norm_step(z, y, None, 0, w_post, gate, gate_sigmoid, alpha, w_next, eps)
+    _matrix(dz, "dz", z.dtype, T, H)
+    _matrix(dh, "dh", z.dtype, T, H)
+    _device_of(z, dz, dh, workspace)
+    f32 = torch.float32
+    g = BlockNormGrads(_new((T, H), z.dtype, dev, stream))
+    if y is not None:
+        g.dy = _new((T, H), z.dtype, dev, stream)
+    if gate is not None:
+        g.dgate = _new((T,) if gate.dim() == 1 else (T, H), gate.dtype, dev, stream)
+    if w_post is not None:
+        g.dw_post = _new((H,), f32, dev, stream)
+    if dh is not None:
+        g.dw_next = _new((H,), f32, dev, stream)
+    if workspace is None:
+        workspace = _new((max(moe_block_norm_bwd_workspace_bytes(T, H), 16),), torch.uint8, dev, stream)
+    gc = BlockNormGradsT(_p(g.dx), _p(g.dy), _p(g.dgate), _p(g.dw_post), _p(g.dw_next))
+    _call_on(dev, stream, "moe_block_norm_bwd", ctypes.byref(step), _p(z), _p(dz), _p(dh), code, T, H, ctypes.byref(gc),
+             _p(workspace), workspace.numel() * workspace.element_size())
+    return g
 
 
 def moe_gather_rows(src: torch.Tensor, idx: torch.Tensor, div: int = 1, n: int | None = None,

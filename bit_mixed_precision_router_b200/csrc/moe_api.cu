@@ -409,6 +409,177 @@ moe_status_t moe_combine(const uint16_t* y_rows, const moe_routing_t* routing, c
   return from_cuda(moe::launch_combine(y_rows, *routing, residual, int(T), int(H), int(k), out, as_stream(stream)));
 }
 
+static bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+static size_t dtype_size(moe_dtype_t dt) { return dt == MOE_F32 ? 4 : 2; }
+static bool dtype_ok(moe_dtype_t dt) { return dt == MOE_BF16 || dt == MOE_F16 || dt == MOE_F32; }
+
+// check_route_shape without k <= E: with dropped pairs a token may choose experts of other ranks
+static moe_status_t check_pairs_shape(int64_t T, int64_t E, int64_t k) {
+  if (T < 0) return MOE_ERR_INVALID_ARG;
+  if (E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || T > INT_MAX / k) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+moe_status_t moe_permute_capacity(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t capacity,
+                                  const moe_routing_t* out, moe_stream_t stream) {
+  if (capacity < 0) return MOE_ERR_INVALID_ARG;
+  const moe_status_t rs = check_pairs_shape(T, E, k);
+  if (rs != MOE_OK) return rs;
+  if (T == 0) return MOE_OK;
+  if (!ids || !out || !out->expert_offsets || !out->sorted_pair || !out->pair_to_row || !out->expert_list)
+    return MOE_ERR_INVALID_ARG;
+  const void* ps[] = {ids, out->expert_offsets, out->sorted_pair, out->pair_to_row, out->expert_list};
+  for (const void* p : ps)
+    if (!aligned_to(p, 4)) return MOE_ERR_MISALIGNED;
+  return from_cuda(moe::launch_permute_capacity(ids, int(T * k), int(E), int(capacity > INT_MAX ? 0 : capacity), *out,
+                                                as_stream(stream)));
+}
+
+// What the four row calls share: shape, the routing's arrays, the element type's alignment.  g.a,
+// g.b and g.out are the caller's; g.b may be NULL.
+static moe_status_t check_rows(moe::RowArgs* g, moe_dtype_t dt, const moe_routing_t* routing, int weighted, int64_t T,
+                               int64_t H, int64_t k) {
+  if (!dtype_ok(dt) || T < 0 || k < 1 || H < 1) return MOE_ERR_INVALID_ARG;
+  if (k > MOE_MAX_TOPK || H > (1 << 20) || T > INT_MAX / k) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!routing || !routing->pair_to_row || (weighted && !routing->topk_w) || !g->a || !g->out) return MOE_ERR_INVALID_ARG;
+  const size_t es = dtype_size(dt);
+  if (!aligned_to(g->a, es) || !aligned_to(g->b, es) || !aligned_to(g->out, es) || !aligned_to(routing->pair_to_row, 4) ||
+      (weighted && !aligned_to(routing->topk_w, 4)) || !aligned_to(g->dw, 4))
+    return MOE_ERR_MISALIGNED;
+  g->w = weighted ? routing->topk_w : nullptr;
+  g->p2r = routing->pair_to_row;
+  g->T = int(T);
+  g->H = int(H);
+  g->k = int(k);
+  return MOE_OK;
+}
+
+moe_status_t moe_sort_rows(const void* x, moe_dtype_t dtype, const moe_routing_t* routing, int weighted, int64_t T,
+                           int64_t H, int64_t k, void* rows, moe_stream_t stream) {
+  moe::RowArgs g = {};
+  g.a = x;
+  g.out = rows;
+  const moe_status_t s = check_rows(&g, dtype, routing, weighted, T, H, k);
+  if (s != MOE_OK || T == 0) return s;
+  return from_cuda(moe::launch_spread_rows(g, dtype, as_stream(stream)));
+}
+
+moe_status_t moe_sort_rows_bwd(const void* d_rows, moe_dtype_t dtype, const moe_routing_t* routing, int weighted,
+                               const void* x, int64_t T, int64_t H, int64_t k, void* dx, float* dw,
+                               moe_stream_t stream) {
+  if (T != 0 && ((x == nullptr) != (dw == nullptr) || (dw && !weighted))) return MOE_ERR_INVALID_ARG;
+  moe::RowArgs g = {};
+  g.a = d_rows;
+  g.b = x;
+  g.out = dx;
+  g.dw = dw;
+  const moe_status_t s = check_rows(&g, dtype, routing, weighted, T, H, k);
+  if (s != MOE_OK || T == 0) return s;
+  return from_cuda(moe::launch_gather_sum(g, dtype, as_stream(stream)));
+}
+
+moe_status_t moe_unsort_rows(const void* rows, moe_dtype_t dtype, const moe_routing_t* routing, int weighted,
+                             const void* residual, int64_t T, int64_t H, int64_t k, void* out, moe_stream_t stream) {
+  moe::RowArgs g = {};
+  g.a = rows;
+  g.b = residual;
+  g.out = out;
+  const moe_status_t s = check_rows(&g, dtype, routing, weighted, T, H, k);
+  if (s != MOE_OK || T == 0) return s;
+  return from_cuda(moe::launch_gather_sum(g, dtype, as_stream(stream)));
+}
+
+moe_status_t moe_unsort_rows_bwd(const void* d_out, moe_dtype_t dtype, const moe_routing_t* routing, int weighted,
+                                 const void* rows, int64_t T, int64_t H, int64_t k, void* d_rows, float* dw,
+                                 moe_stream_t stream) {
+  if (T != 0 && ((rows == nullptr) != (dw == nullptr) || (dw && !weighted))) return MOE_ERR_INVALID_ARG;
+  moe::RowArgs g = {};
+  g.a = d_out;
+  g.b = rows;
+  g.out = d_rows;
+  g.dw = dw;
+  const moe_status_t s = check_rows(&g, dtype, routing, weighted, T, H, k);
+  if (s != MOE_OK || T == 0) return s;
+  return from_cuda(moe::launch_spread_rows(g, dtype, as_stream(stream)));
+}
+
+moe_status_t moe_route_topk_bwd(const float* dw, const moe_routing_t* routing, int64_t T, int64_t E, int64_t k,
+                                float* d_logits, moe_stream_t stream) {
+  const moe_status_t rs = check_pairs_shape(T, E, k);
+  if (rs != MOE_OK) return rs;
+  if (T == 0) return MOE_OK;
+  if (!dw || !d_logits || !routing || !routing->topk_ids || !routing->topk_w) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(dw, 4) || !aligned_to(d_logits, 4) || !aligned_to(routing->topk_ids, 4) ||
+      !aligned_to(routing->topk_w, 4))
+    return MOE_ERR_MISALIGNED;
+  return from_cuda(moe::launch_route_bwd(dw, routing->topk_w, routing->topk_ids, int(T), int(E), int(k), d_logits,
+                                         as_stream(stream)));
+}
+
+static moe_status_t check_norm(const moe_block_norm_t* b, moe_dtype_t dt, int64_t T, int64_t H) {
+  if (!b || !dtype_ok(dt) || T < 0 || H < 1) return MOE_ERR_INVALID_ARG;
+  if (!(b->eps > 0.0f) || b->eps > 1e30f || !(b->alpha >= -1e30f && b->alpha <= 1e30f)) return MOE_ERR_INVALID_ARG;
+  if (b->gate_mode != MOE_GATE_NONE && b->gate_mode != MOE_GATE_TOKEN && b->gate_mode != MOE_GATE_FULL)
+    return MOE_ERR_INVALID_ARG;
+  if (H > 16384 || T > INT_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return MOE_OK;
+  if ((b->gate_mode == MOE_GATE_NONE) != (b->gate == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!b->y && (b->w_post || b->gate || b->pair_to_row)) return MOE_ERR_INVALID_ARG;
+  if (b->pair_to_row) {
+    if (b->k < 1) return MOE_ERR_INVALID_ARG;
+    if (b->k > MOE_MAX_TOPK || T > INT_MAX / b->k) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned_to(b->pair_to_row, 4) || !aligned_to(b->topk_w, 4)) return MOE_ERR_MISALIGNED;
+  }
+  const size_t es = dtype_size(dt);
+  if (!aligned_to(b->y, es) || !aligned_to(b->w_post, es) || !aligned_to(b->w_next, es) ||
+      !aligned_to(b->gate, b->gate_mode == MOE_GATE_TOKEN ? 4 : es))
+    return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+moe_status_t moe_block_norm(const moe_block_norm_t* step, const void* x, moe_dtype_t dtype, int64_t T, int64_t H, void* z,
+                            void* h, moe_stream_t stream) {
+  const moe_status_t s = check_norm(step, dtype, T, H);
+  if (s != MOE_OK || T == 0) return s;
+  if (!x || (z != nullptr) != (step->y != nullptr) || (h != nullptr) != (step->w_next != nullptr) || (!z && !h))
+    return MOE_ERR_INVALID_ARG;
+  const size_t es = dtype_size(dtype);
+  if (!aligned_to(x, es) || !aligned_to(z, es) || !aligned_to(h, es)) return MOE_ERR_MISALIGNED;
+  return from_cuda(moe::launch_block_norm(*step, x, int(T), int(H), dtype, z, h, as_stream(stream)));
+}
+
+size_t moe_block_norm_bwd_workspace_bytes(int64_t T, int64_t H) {
+  if (T < 0 || H < 1) return 0;
+  return moe::block_norm_bwd_workspace_bytes(T, H);
+}
+
+moe_status_t moe_block_norm_bwd(const moe_block_norm_t* step, const void* z, const void* dz, const void* dh,
+                                moe_dtype_t dtype, int64_t T, int64_t H, const moe_block_norm_grads_t* grads,
+                                void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  const moe_status_t s = check_norm(step, dtype, T, H);
+  if (s != MOE_OK) return s;
+  if (!grads) return MOE_ERR_INVALID_ARG;
+  const moe_block_norm_grads_t& g = *grads;
+  if (!aligned_to(g.dw_post, 4) || !aligned_to(g.dw_next, 4)) return MOE_ERR_MISALIGNED;
+  if (T == 0) {  // sums over no tokens
+    for (float* w : {g.dw_post, g.dw_next})
+      if (w && cudaMemsetAsync(w, 0, size_t(H) * sizeof(float), as_stream(stream)) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (step->pair_to_row || (!dz && !dh) || (dh && (!z || !step->w_next))) return MOE_ERR_INVALID_ARG;
+  if ((g.dy && !step->y) || (g.dgate && !step->gate) || (g.dw_post && !step->w_post) || (g.dw_next && !dh))
+    return MOE_ERR_INVALID_ARG;
+  const size_t es = dtype_size(dtype);
+  for (const void* p : {z, dz, dh, static_cast<const void*>(g.dx), static_cast<const void*>(g.dy)})
+    if (!aligned_to(p, es)) return MOE_ERR_MISALIGNED;
+  if (!aligned_to(g.dgate, step->gate_mode == MOE_GATE_TOKEN ? 4 : es)) return MOE_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < moe::block_norm_bwd_workspace_bytes(T, H)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MOE_ERR_MISALIGNED;
+  return from_cuda(moe::launch_block_norm_bwd(*step, z, dz, dh, int(T), int(H), dtype, g, workspace, as_stream(stream)));
+}
+
 moe_status_t moe_gather_rows(const uint16_t* src, const int32_t* idx, int64_t n, int64_t div, int64_t H,
                              uint16_t* dst, moe_stream_t stream) {
   if (n < 0 || div < 1 || H < 8) return MOE_ERR_INVALID_ARG;

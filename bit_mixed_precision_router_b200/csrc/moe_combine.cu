@@ -15,6 +15,7 @@ __global__ void k_combine(const uint16_t* __restrict__ y, const int32_t* __restr
   for (int j = 0; j < k; ++j) {
     const float wj = w[size_t(t) * k + j];
     const int row = p2r[size_t(t) * k + j];
+    if (row < 0) continue;  // a dropped pair (moe_permute_capacity)
     const uint4 v = *reinterpret_cast<const uint4*>(y + size_t(row) * H + h);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -90,6 +90,34 @@ cudaError_t launch_gather_rows_by(const uint16_t* src, const int32_t* idx, int n
                                   cudaStream_t st);
 cudaError_t launch_ids_from_counts(const int32_t* counts, int S, int El, int32_t* ids, cudaStream_t st);
 
+// Rows sorted by expert and back (moe_rows.cu).  a: token rows [T][H]; out and b: see each call;
+// w: fp32 [T*k] or NULL (weight 1); p2r: row of each pair, negative where it has none; dw: fp32 [T*k]
+// or NULL (no dot products).
+struct RowArgs {
+  const void* a;
+  const void* b;
+  const float* w;
+  const int32_t* p2r;
+  int T, H, k;
+  void* out;
+  float* dw;
+};
+// out[p2r[p]] = w_p a[t]; dw_p = <a[t], b[p2r[p]]>
+cudaError_t launch_spread_rows(const RowArgs& g, moe_dtype_t dt, cudaStream_t st);
+// out[t] = sum_j w_p a[p2r[p]] + b[t] (b NULL: nothing); with dw: b is not added, dw_p = <a[p2r[p]], b[t]>
+cudaError_t launch_gather_sum(const RowArgs& g, moe_dtype_t dt, cudaStream_t st);
+cudaError_t launch_route_bwd(const float* dw, const float* w, const int32_t* ids, int T, int E, int k, float* dlogits,
+                             cudaStream_t st);
+cudaError_t launch_permute_capacity(const int32_t* ids, int P, int E, int cap, const moe_routing_t& out,
+                                    cudaStream_t st);
+
+// Norms around a block (moe_norm.cu).
+cudaError_t launch_block_norm(const moe_block_norm_t& b, const void* x, int T, int H, moe_dtype_t dt, void* z, void* h,
+                              cudaStream_t st);
+size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H);
+cudaError_t launch_block_norm_bwd(const moe_block_norm_t& b, const void* z, const void* dz, const void* dh, int T, int H,
+                                  moe_dtype_t dt, const moe_block_norm_grads_t& g, void* ws, cudaStream_t st);
+
 cudaError_t launch_combine(const uint16_t* y_rows, const moe_routing_t& r, const uint16_t* residual, int T,
                            int H, int k, uint16_t* out, cudaStream_t st);
 

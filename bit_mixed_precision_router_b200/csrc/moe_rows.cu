@@ -1,0 +1,409 @@
+// Tokens sorted by expert and back, with routing weights, and the gradients.  With p = t*k + j
+// a (token, slot) pair, r(p) = pair_to_row[p] its row (negative: the pair was dropped and has no
+// row) and w_p its weight (1 where the call is unweighted):
+//   sort      rows[r(p)] = w_p x[t]                      back      out[t] = sum_j w_p rows[r(p)] (+ residual[t])
+//   d sort    dx[t] = sum_j w_p drows[r(p)]              d back    drows[r(p)] = w_p dout[t]
+//             dw_p = <drows[r(p)], x[t]>                           dw_p = <dout[t], rows[r(p)]>
+// Each gradient is the other direction plus one dot product per pair, so two kernels cover all four:
+//   k_spread  token-major: reads a[t] once, writes its k rows (and reads k rows for the dots);
+//   k_gather  token-major: reads k rows, writes one (and reads one more for the dots).
+// Token-major needs no atomics (a token's k pairs belong to one CTA) and reads the token's row once.
+// Sums run in fp32 in slot order, each result rounded once to the element type; the dots stay fp32.
+// Bound by HBM: (k + 1) rows per token, (2k + 1) or (k + 2) with the dots.
+//   k_route_bwd  the gradient of the softmax over the k chosen logits.
+//   k_permute_cap  the stable counting sort behind it, with dropped pairs and a row limit per expert.
+#include <cooperative_groups.h>
+
+#include "moe_internal.h"
+#include "moe_vec.cuh"
+
+namespace moe {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kRowThreads = 256;
+constexpr int kSlots = 8;  // rows of a token in flight per thread
+
+template <typename T, int V, bool DOT>
+__global__ void __launch_bounds__(kRowThreads) k_spread(const T* a, const T* __restrict__ b, const float* __restrict__ w,
+                                                        const int32_t* __restrict__ p2r, int H, int k,
+                                                        T* __restrict__ rows, float* __restrict__ dw) {
+  __shared__ float red[kSlots * 32];
+  const int t = blockIdx.x, nv = H / V;
+  const T* arow = a + size_t(t) * H;
+  const int step = DOT ? int(blockDim.x) : int(blockDim.x * gridDim.y);
+  const int v0 = DOT ? int(threadIdx.x) : int(blockIdx.y * blockDim.x + threadIdx.x);
+  for (int j0 = 0; j0 < k; j0 += kSlots) {
+    int row[kSlots];
+    float wj[kSlots], dot[kSlots];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      const size_t p = size_t(t) * k + j0 + j;
+      row[j] = j0 + j < k ? p2r[p] : -1;
+      wj[j] = w && j0 + j < k ? w[p] : 1.0f;
+      dot[j] = 0.0f;
+    }
+    for (int v = v0; v < nv; v += step) {
+      Pack<T, V> bv[kSlots];
+      const Pack<T, V> av = load_vec<T, V>(arow, v);
+      if (DOT) {
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j)
+          if (row[j] >= 0) bv[j] = load_vec_once<T, V>(b + size_t(row[j]) * H, v);
+      }
+      float f[V];
+      av.unpack(f);
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        if (row[j] < 0) continue;
+        if (DOT) {
+          float g[V];
+          bv[j].unpack(g);
+#pragma unroll
+          for (int i = 0; i < V; ++i) dot[j] = fmaf(f[i], g[i], dot[j]);
+        }
+        if (w) {
+          float o[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] = wj[j] * f[i];
+          store_vec(rows + size_t(row[j]) * H, v, Pack<T, V>::of(o));
+        } else {
+          store_vec(rows + size_t(row[j]) * H, v, av);
+        }
+      }
+    }
+    if (DOT) {
+      block_sum<kSlots>(dot, red);
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (threadIdx.x == j && j0 + j < k) dw[size_t(t) * k + j0 + j] = dot[j];
+      __syncthreads();
+    }
+  }
+}
+
+// KB: slots unrolled (k <= KB).
+template <typename T, int V, bool DOT, int KB>
+__global__ void __launch_bounds__(kRowThreads) k_gather(const T* __restrict__ rows, const T* x, const float* __restrict__ w,
+                                                        const int32_t* __restrict__ p2r, int H, int k, T* out,
+                                                        float* __restrict__ dw) {
+  __shared__ float red[KB * 32];
+  __shared__ int srow[KB];
+  __shared__ float sw[KB];
+  const int t = blockIdx.x, nv = H / V;
+  if (threadIdx.x < KB) {
+    const bool in = int(threadIdx.x) < k;
+    const size_t p = size_t(t) * k + threadIdx.x;
+    srow[threadIdx.x] = in ? p2r[p] : -1;
+    sw[threadIdx.x] = in && w ? w[p] : 1.0f;
+  }
+  __syncthreads();
+  float dot[KB];
+#pragma unroll
+  for (int j = 0; j < KB; ++j) dot[j] = 0.0f;
+  const int step = DOT ? int(blockDim.x) : int(blockDim.x * gridDim.y);
+  for (int v = DOT ? int(threadIdx.x) : int(blockIdx.y * blockDim.x + threadIdx.x); v < nv; v += step) {
+    float acc[V], xf[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = xf[i] = 0.0f;
+    Pack<T, V> xv;
+    if (x) xv = load_vec<T, V>(x + size_t(t) * H, v);
+    if (DOT) xv.unpack(xf);
+#pragma unroll
+    for (int j0 = 0; j0 < KB; j0 += kSlots) {
+      if (j0 >= k) break;
+      Pack<T, V> r[kSlots];
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (srow[j0 + j] >= 0) r[j] = load_vec_once<T, V>(rows + size_t(srow[j0 + j]) * H, v);
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        if (srow[j0 + j] < 0) continue;
+        float f[V];
+        r[j].unpack(f);
+        const float wj = sw[j0 + j];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
+        if (DOT) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) dot[j0 + j] = fmaf(xf[i], f[i], dot[j0 + j]);
+        }
+      }
+    }
+    if (!DOT && x) {  // the residual, added last
+      xv.unpack(xf);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += xf[i];
+    }
+    store_vec(out + size_t(t) * H, v, Pack<T, V>::of(acc));
+  }
+  if (DOT) {
+    block_sum<KB>(dot, red);
+#pragma unroll
+    for (int j = 0; j < KB; ++j)
+      if (threadIdx.x == j && j < k) dw[size_t(t) * k + j] = dot[j];
+  }
+}
+
+// One warp per token: dl_j = w_j (dw_j - sum_i w_i dw_i), scattered into a row of zeros.  Pairs
+// are added in slot order by one lane, so an expert chosen twice gets both parts, in one order.
+constexpr int kRouteWarps = 4;
+__global__ void __launch_bounds__(32 * kRouteWarps) k_route_bwd(const float* __restrict__ dw, const float* __restrict__ w,
+                                                                const int32_t* __restrict__ ids, int T, int E, int k,
+                                                                float* __restrict__ dl) {
+  extern __shared__ float smem_f[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kRouteWarps + warp;
+  if (t >= T) return;
+  float* row = smem_f + warp * E;
+  for (int e = lane; e < E; e += 32) row[e] = 0.0f;
+  const size_t p = size_t(t) * k + lane;
+  const float wj = lane < k ? w[p] : 0.0f, d = lane < k ? dw[p] : 0.0f;
+  const int id = lane < k ? ids[p] : -1;
+  const float g = wj * (d - warp_sum(wj * d));
+  __syncwarp();
+  for (int j = 0; j < k; ++j) {
+    if (lane == j && id >= 0 && id < E) row[id] += g;
+    __syncwarp();
+  }
+  for (int e = lane; e < E; e += 32) dl[size_t(t) * E + e] = row[e];
+}
+
+// ---------------------------------------------------------------- permutation with dropped pairs
+// A stable counting sort of P pairs by expert over one cluster of C CTAs (C = 1 for small P): warp
+// q of the cluster (CTA rank * NW + warp) owns pairs [q P / (C NW), (q+1) P / (C NW)).
+//   1. each warp counts its pairs per expert (bin E: ids outside 0..E-1);
+//   2. per expert, the counts of earlier warps (own CTA) and earlier CTAs (distributed shared
+//      memory) give the pair's index inside its expert; the kept totals give the expert's first row;
+//   3. a pair whose index is below the limit takes row first + index, any other is dropped: it gets
+//      row -1 and follows the last kept row in sorted_pair, in ascending order.  The number of
+//      dropped pairs ahead of a warp follows from the same counts.
+// `cnt` is [NW][E + 1] ints of shared memory.
+constexpr int kPermThreads = 1024;
+constexpr int kPermCntInts = 8192;  // 32 KiB of counts: NW = min(32, 8192 / (E + 1))
+
+__global__ void __launch_bounds__(kPermThreads) k_permute_cap(const int32_t* __restrict__ ids, int P, int E, int cap,
+                                                              int NW, int C, moe_routing_t out) {
+  __shared__ int cnt[kPermCntInts];
+  __shared__ int tot[MOE_MAX_EXPERTS + 1];   // this CTA's pairs per bin
+  __shared__ int base[MOE_MAX_EXPERTS + 1];  // pairs of the bin in earlier CTAs, then the first row
+  __shared__ int dropped[33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwb = blockDim.x >> 5;
+  const int B = E + 1;
+  const int rank = C > 1 ? int(cg::this_cluster().block_rank()) : 0;
+  for (int i = threadIdx.x; i < NW * B; i += blockDim.x) cnt[i] = 0;
+  __syncthreads();
+  const int64_t q = int64_t(rank) * NW + warp, Q = int64_t(C) * NW;
+  const int beg = int(q * P / Q), end = int((q + 1) * P / Q);
+  int* mine = cnt + warp * B;
+  if (warp < NW) {
+    for (int p0 = beg; p0 < end; p0 += 32) {
+      const int p = p0 + lane;
+      int id = -1;
+      if (p < end) {
+        id = ids[p];
+        id = id >= 0 && id < E ? id : E;
+      }
+      const unsigned peers = __match_any_sync(0xffffffffu, id);
+      if (id >= 0 && (__ffs(peers) - 1) == lane) mine[id] += __popc(peers);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < B; e += blockDim.x) {
+    int run = 0;
+    for (int w = 0; w < NW; ++w) {
+      const int c = cnt[w * B + e];
+      cnt[w * B + e] = run;
+      run += c;
+    }
+    tot[e] = run;
+  }
+  if (C > 1)
+    cg::this_cluster().sync();
+  else
+    __syncthreads();
+  // pairs of bin e in earlier CTAs, and in all
+  const int limit = cap > 0 ? cap : 0x7fffffff;
+  int all_of[2] = {0, 0};  // B <= 1025 bins over 1024 threads
+  for (int i = 0, e = threadIdx.x; e < B; e += blockDim.x, ++i) {
+    int before = 0, all = 0;
+    for (int c = 0; c < C; ++c) {
+      const int v = C > 1 ? *cg::this_cluster().map_shared_rank(&tot[e], c) : tot[e];
+      before += c < rank ? v : 0;
+      all += v;
+    }
+    base[e] = before;
+    all_of[i] = all;
+  }
+  if (C > 1)
+    cg::this_cluster().sync();  // every CTA has read the totals; from here each is on its own
+  else
+    __syncthreads();
+  for (int i = 0, e = threadIdx.x; e < B; e += blockDim.x, ++i) tot[e] = all_of[i];
+  __syncthreads();
+  // dropped pairs ahead of each warp: its own earlier pairs past the limit, bin E whole
+  for (int w = warp; w < NW; w += nwb) {
+    int s = 0;
+    for (int e = lane; e < B; e += 32) {
+      const int c = base[e] + cnt[w * B + e];
+      s += e == E ? c : max(0, c - limit);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0) dropped[w] = s;
+  }
+  __syncthreads();
+  // cnt: index inside the expert of the warp's next pair; base: first row; dropped[32]: kept rows
+  for (int i = threadIdx.x; i < NW * B; i += blockDim.x) cnt[i] += base[i % B];
+  __syncthreads();
+  if (warp == 0) {
+    const int per = (E + 31) / 32;
+    const int b = min(E, lane * per), en = min(E, b + per);
+    int sum = 0, act = 0;
+    for (int e = b; e < en; ++e) {
+      sum += min(tot[e], limit);
+      act += tot[e] > 0;
+    }
+    int isum = sum, iact = act;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v1 = __shfl_up_sync(0xffffffffu, isum, d), v2 = __shfl_up_sync(0xffffffffu, iact, d);
+      if (lane >= d) {
+        isum += v1;
+        iact += v2;
+      }
+    }
+    int run = isum - sum, pos = iact - act;
+    for (int e = b; e < en; ++e) {
+      const int n = min(tot[e], limit);
+      base[e] = run;
+      if (rank == 0) {
+        out.expert_offsets[e] = run;
+        if (n > 0) out.expert_list[1 + pos] = e;
+      }
+      pos += n > 0;
+      run += n;
+    }
+    if (lane == 31) {
+      dropped[32] = isum;
+      if (rank == 0) {
+        out.expert_offsets[E] = isum;
+        out.expert_list[0] = iact;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp >= NW) return;
+  const int kept_rows = dropped[32];
+  int drop_at = kept_rows + dropped[warp];
+  const unsigned lt = (1u << lane) - 1u;
+  for (int p0 = beg; p0 < end; p0 += 32) {
+    const int p = p0 + lane;
+    int id = -1;
+    if (p < end) {
+      id = ids[p];
+      id = id >= 0 && id < E ? id : E;
+    }
+    const unsigned peers = __match_any_sync(0xffffffffu, id);
+    int idx = 0;
+    if (id >= 0) idx = mine[id] + __popc(peers & lt);
+    __syncwarp();
+    if (id >= 0 && (__ffs(peers) - 1) == lane) mine[id] += __popc(peers);
+    __syncwarp();
+    const bool keep = id >= 0 && id < E && idx < limit;
+    const unsigned lost = __ballot_sync(0xffffffffu, id >= 0 && !keep);
+    if (id >= 0) {
+      const int row = keep ? base[id] + idx : drop_at + __popc(lost & lt);
+      out.sorted_pair[row] = p;
+      out.pair_to_row[p] = keep ? row : -1;
+    }
+    drop_at += __popc(lost);
+  }
+}
+
+// ---------------------------------------------------------------- launchers
+int row_threads(int nv) {  // as many threads as the row has vectors, at most kRowThreads
+  const int t = (nv + 31) / 32 * 32;
+  return t < kRowThreads ? t : kRowThreads;
+}
+
+template <typename T, int V>
+cudaError_t spread(const RowArgs& g, cudaStream_t st) {
+  const int nv = g.H / V, threads = row_threads(nv);
+  const T *a = static_cast<const T*>(g.a), *b = static_cast<const T*>(g.b);
+  T* out = static_cast<T*>(g.out);
+  if (g.dw) {
+    k_spread<T, V, true><<<unsigned(g.T), threads, 0, st>>>(a, b, g.w, g.p2r, g.H, g.k, out, g.dw);
+  } else {
+    const dim3 grid(unsigned(g.T), unsigned((nv + threads - 1) / threads));
+    k_spread<T, V, false><<<grid, threads, 0, st>>>(a, nullptr, g.w, g.p2r, g.H, g.k, out, nullptr);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T, int V, bool DOT>
+cudaError_t gather_of(const RowArgs& g, cudaStream_t st) {
+  const int nv = g.H / V, threads = row_threads(nv);
+  const T *a = static_cast<const T*>(g.a), *b = static_cast<const T*>(g.b);
+  T* out = static_cast<T*>(g.out);
+  const dim3 grid(unsigned(g.T), DOT ? 1u : unsigned((nv + threads - 1) / threads));
+  if (g.k <= kSlots)
+    k_gather<T, V, DOT, kSlots><<<grid, threads, 0, st>>>(a, b, g.w, g.p2r, g.H, g.k, out, g.dw);
+  else
+    k_gather<T, V, DOT, MOE_MAX_TOPK><<<grid, threads, 0, st>>>(a, b, g.w, g.p2r, g.H, g.k, out, g.dw);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t rows_of(const RowArgs& g, bool is_spread, cudaStream_t st) {
+  constexpr int V = vec_width<T>();
+  // 128-bit accesses where every row starts on 16 bytes; else one element at a time
+  const bool wide = g.H % V == 0 && vec_aligned(g.a) && vec_aligned(g.b) && vec_aligned(g.out);
+  if (is_spread) return wide ? spread<T, V>(g, st) : spread<T, 1>(g, st);
+  if (g.dw) return wide ? gather_of<T, V, true>(g, st) : gather_of<T, 1, true>(g, st);
+  return wide ? gather_of<T, V, false>(g, st) : gather_of<T, 1, false>(g, st);
+}
+
+cudaError_t rows_any(const RowArgs& g, moe_dtype_t dt, bool is_spread, cudaStream_t st) {
+  if (dt == MOE_BF16) return rows_of<__nv_bfloat16>(g, is_spread, st);
+  if (dt == MOE_F16) return rows_of<__half>(g, is_spread, st);
+  return rows_of<float>(g, is_spread, st);
+}
+
+}  // namespace
+
+cudaError_t launch_spread_rows(const RowArgs& g, moe_dtype_t dt, cudaStream_t st) { return rows_any(g, dt, true, st); }
+cudaError_t launch_gather_sum(const RowArgs& g, moe_dtype_t dt, cudaStream_t st) { return rows_any(g, dt, false, st); }
+
+cudaError_t launch_route_bwd(const float* dw, const float* w, const int32_t* ids, int T, int E, int k, float* dlogits,
+                             cudaStream_t st) {
+  k_route_bwd<<<unsigned((T + kRouteWarps - 1) / kRouteWarps), 32 * kRouteWarps, kRouteWarps * E * sizeof(float), st>>>(
+      dw, w, ids, T, E, k, dlogits);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_permute_capacity(const int32_t* ids, int P, int E, int cap, const moe_routing_t& out,
+                                    cudaStream_t st) {
+  const int most = kPermCntInts / (E + 1) < 32 ? kPermCntInts / (E + 1) : 32;
+  const int C = P > 4096 ? 8 : 1;  // pairs enough for several CTAs
+  const int want = (P + 32 * C - 1) / (32 * C);
+  const int NW = want < most ? want : most;
+  // the bins are walked by all threads, two per thread at most
+  const int bins = ((E + 2) / 2 + 31) / 32 * 32;
+  const int threads = 32 * NW > bins ? 32 * NW : bins;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(C));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(C);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_permute_cap, ids, P, E, cap, NW, C, out);
+}
+
+}  // namespace moe

@@ -425,12 +425,140 @@ moe_status_t moe_grouped_ffn_w4a4(const uint16_t* x, const moe_routing_t* routin
 
 /* Routing-weighted combine [ExactMoE: the selected experts' outputs weighted by the
  * unchanged routing weights]: out[t] = bf16( sum_{j<k} topk_w[t*k+j] *
- * y_rows[pair_to_row[t*k+j]] (+ residual[t]) ), fp32 accumulation in slot order j.
+ * y_rows[pair_to_row[t*k+j]] (+ residual[t]) ), fp32 accumulation in slot order j; a
+ * negative pair_to_row adds nothing.
  *   y_rows bf16 [T*k][H];  residual bf16 [T][H] or NULL;  out bf16 [T][H] (may alias residual).
  * Requires H % 8 == 0.  Deterministic. */
 moe_status_t moe_combine(const uint16_t* y_rows, const moe_routing_t* routing,
                          const uint16_t* residual, int64_t T, int64_t H, int64_t k,
                          uint16_t* out, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Tokens sorted by expert and back, with routing weights, and the gradients
+ *
+ * p = t*k + j is a (token, slot) pair, r(p) = pair_to_row[p] its row; r(p) < 0 marks a pair
+ * without a row (dropped: nothing is read or written for it).  w_p = topk_w[p] where `weighted`
+ * is nonzero, else 1.  Element types: moe_dtype_t; sums in fp32 in slot order, rounded once.
+ * Of the routing only pair_to_row is read (and topk_w where weighted), 4-byte aligned.
+ * Row buffers need only their element's alignment: 128-bit accesses are used when they start on
+ * 16 bytes and H is a multiple of 16 bytes, else single elements.  Rows that no pair refers to are
+ * left as they are.  1 <= H <= 2^20, 1 <= k <= MOE_MAX_TOPK.  Outputs must not overlap inputs,
+ * except that out may be residual.  Deterministic.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the operators below. */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype_t;
+
+/* moe_permute with dropped pairs.  A pair is dropped if its id is outside 0..E-1 (padding, or an
+ * expert of another rank), or if `capacity` > 0 and `capacity` pairs of smaller index have the
+ * same id.  Kept pairs are sorted stably by expert; expert_offsets, expert_list and pair_to_row
+ * describe them (expert_offsets[E] rows).  Dropped pairs get pair_to_row -1 and follow the last row
+ * in sorted_pair, in ascending order (so sorted_pair stays a permutation).  topk_ids and topk_w are
+ * not touched.  The routing serves moe_grouped_ffn (rows from expert_offsets[E] on are not
+ * computed), the calls below and moe_combine (a dropped pair adds nothing); not
+ * moe_grouped_ffn_w4a4, whose activation scale spans all T*k rows.
+ *   ids int32 [T*k], 4-byte aligned; capacity >= 0 (0: no limit); 1 <= E <= MOE_MAX_EXPERTS,
+ *   1 <= k <= MOE_MAX_TOPK (k may exceed E).  T = 0: nothing is written. */
+moe_status_t moe_permute_capacity(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t capacity,
+                                  const moe_routing_t* out, moe_stream_t stream);
+
+/* rows[r(p)] = w_p x[t].   x [T][H]; rows [>= rows in use][H]. */
+moe_status_t moe_sort_rows(const void* x, moe_dtype_t dtype, const moe_routing_t* routing, int weighted, int64_t T,
+                           int64_t H, int64_t k, void* rows, moe_stream_t stream);
+
+/* Gradient of moe_sort_rows: dx[t] = sum_j w_p d_rows[r(p)]; dw[p] = <d_rows[r(p)], x[t]> (0 for a
+ * dropped pair), fp32 [T*k], 4-byte aligned.  x and dw are both NULL if the weights' gradient is
+ * not wanted, and must be if the call is unweighted. */
+moe_status_t moe_sort_rows_bwd(const void* d_rows, moe_dtype_t dtype, const moe_routing_t* routing, int weighted,
+                               const void* x, int64_t T, int64_t H, int64_t k, void* dx, float* dw,
+                               moe_stream_t stream);
+
+/* out[t] = sum_j w_p rows[r(p)] (+ residual[t]; NULL: nothing).  A token without rows gets its
+ * residual, or zeros. */
+moe_status_t moe_unsort_rows(const void* rows, moe_dtype_t dtype, const moe_routing_t* routing, int weighted,
+                             const void* residual, int64_t T, int64_t H, int64_t k, void* out, moe_stream_t stream);
+
+/* Gradient of moe_unsort_rows (the residual's is d_out itself): d_rows[r(p)] = w_p d_out[t];
+ * dw[p] = <d_out[t], rows[r(p)]> (0 for a dropped pair).  rows and dw are both NULL if the weights'
+ * gradient is not wanted, and must be if the call is unweighted. */
+moe_status_t moe_unsort_rows_bwd(const void* d_out, moe_dtype_t dtype, const moe_routing_t* routing, int weighted,
+                                 const void* rows, int64_t T, int64_t H, int64_t k, void* d_rows, float* dw,
+                                 moe_stream_t stream);
+
+/* Gradient of the routing weights' softmax over each token's k chosen logits, as rows over all
+ * experts: d_logits[t][e] = sum over slots j with topk_ids[p] = e of w_p (dw[p] - sum_i w_i dw_i),
+ * 0 for experts not chosen.  An id outside 0..E-1 has no column (its weight still counts in the
+ * softmax).   dw fp32 [T*k];  d_logits fp32 [T][E];  routing: topk_ids and topk_w.  Pointers
+ * 4-byte aligned.  Limits on E and k as for moe_permute_capacity. */
+moe_status_t moe_route_topk_bwd(const float* dw, const moe_routing_t* routing, int64_t T, int64_t E, int64_t k,
+                                float* d_logits, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Norms before and after a block, fused with its gate and residual scale
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_TOKEN = 1, /* fp32 [T], one value per token */
+  MOE_GATE_FULL = 2   /* [T][H] of the call's element type */
+} moe_gate_t;
+
+/* What stands between a block and the next.  Per token, in fp32 (RMS norms):
+ *   n = y * rsqrt(mean(y^2) + eps) * w_post   (n = y if w_post is NULL)
+ *   z = x + alpha * a * n                     a = gate, sigmoid(gate) if gate_sigmoid, 1 without a gate
+ *   h = z * rsqrt(mean(z^2) + eps) * w_next
+ * y is the block's output [T][H]; or, if pair_to_row is not NULL, its routed rows, and the token's
+ * y is sum_j topk_w[p] * y[pair_to_row[p]] over its k slots (negative: no row; topk_w NULL: weight
+ * 1).  y NULL: no block, h is the norm of x alone.  w_post, w_next: [H] of the element type. */
+typedef struct {
+  const void* y;
+  const int32_t* pair_to_row; /* [T*k] or NULL */
+  const float* topk_w;        /* [T*k] or NULL */
+  int64_t k;                  /* used with pair_to_row only */
+  const void* w_post;
+  moe_gate_t gate_mode;
+  const void* gate;
+  int gate_sigmoid;
+  float alpha;
+  const void* w_next;
+  float eps;
+} moe_block_norm_t;
+
+/* z and h of the step above, each rounded once to the element type (h from the unrounded z).
+ * z: needed if y is given, else not written (NULL).  h: needed if w_next is given, else NULL.  At
+ * least one of the two.  z may be x (in place); no other overlap of outputs with inputs or each other.
+ * eps > 0; 1 <= H <= 16384.  Row buffers and weights: their element's alignment (128-bit accesses as
+ * for the calls above); gate per token, pair_to_row and topk_w: 4 bytes.  |y|, |z| < 2^56 keep the
+ * sums of squares finite.  Deterministic. */
+moe_status_t moe_block_norm(const moe_block_norm_t* step, const void* x, moe_dtype_t dtype, int64_t T, int64_t H, void* z,
+                            void* h, moe_stream_t stream);
+
+/* Gradients of moe_block_norm; each may be NULL (not wanted). */
+typedef struct {
+  void* dx;       /* [T][H] */
+  void* dy;       /* [T][H] (with routed rows the gradient of the combined y: step->y must be that y) */
+  void* dgate;    /* fp32 [T] or [T][H], as the gate */
+  float* dw_post; /* fp32 [H] */
+  float* dw_next; /* fp32 [H] */
+} moe_block_norm_grads_t;
+
+size_t moe_block_norm_bwd_workspace_bytes(int64_t T, int64_t H);
+
+/* Gradients given dz [T][H] (NULL: zero) and dh [T][H] (NULL: zero; needs step->w_next), at least one
+ * of them, from z as the forward call wrote it (x itself for a step without a block), and step->y,
+ * which must be the combined y [T][H] (pair_to_row NULL).  Statistics are recomputed from the rows:
+ *   d = dz + r (w_next dh) - z r^3 <z, w_next dh> / H,  r = rsqrt(mean(z^2) + eps)      = dx
+ *   dn = alpha a d,  dy = q (w_post dn) - y q^3 <y, w_post dn> / H,  q = rsqrt(mean(y^2) + eps)
+ *   dgate = alpha a' d n (summed over the token's row for a gate per token)
+ *   dw_post = sum_t dn y q,  dw_next = sum_t dh z r      (fp32, in an order fixed by T, H and the types)
+ * z may be NULL if dh is.  Outputs must not overlap inputs, except that dx may be dz.  A gradient that
+ * the step does not have (dy without y, dgate without gate, dw_post without w_post, dw_next without dh)
+ * must be NULL.  Workspace: at least moe_block_norm_bwd_workspace_bytes(T, H), 16-byte aligned, contents
+ * need not be initialised; calls that overlap on one workspace race.  T = 0 writes zeros to dw_post
+ * and dw_next. */
+moe_status_t moe_block_norm_bwd(const moe_block_norm_t* step, const void* z, const void* dz, const void* dh,
+                                moe_dtype_t dtype, int64_t T, int64_t H, const moe_block_norm_grads_t* grads,
+                                void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Expert parallelism: the device side of the exchange [ExactMoE: every selected expert
