@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 FMT_W4G128, FMT_BITPLANE8, FMT_NVFP4 = 0, 1, 2
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype_t
+ACT_NONE, ACT_SWIGLU = 0, 1
 GATE_NONE, GATE_TOKEN, GATE_FULL = 0, 1, 2
 MAX_EXPERTS, MAX_TOPK = 1024, 32
 
@@ -43,6 +44,10 @@ class ExpertsT(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int), ("w13", ctypes.c_void_p), ("w13_scale", ctypes.c_void_p),
                 ("w2", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p), ("w13_gscale", ctypes.c_void_p),
                 ("w2_gscale", ctypes.c_void_p)]
+
+
+class LinearT(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int), ("w", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("gscale", ctypes.c_void_p)]
 
 
 class BlockNormT(ctypes.Structure):
@@ -102,6 +107,8 @@ _SIGS = {
     "moe_grouped_ffn_w4a4": ([_vp, ctypes.POINTER(RoutingT), ctypes.POINTER(ExpertsT), _vp, _i64, _i64, _i64, _i64,
                               _i64, _vp, _vp, _sz, _vp], ctypes.c_int),
     "moe_combine": ([_vp, ctypes.POINTER(RoutingT), _vp, _i64, _i64, _i64, _vp, _vp], ctypes.c_int),
+    "moe_linear_w4": ([_vp, _i64, ctypes.c_int, ctypes.POINTER(LinearT), _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp,
+                       _i64, ctypes.c_int, _vp], ctypes.c_int),
     "moe_permute_capacity": ([_vp, _i64, _i64, _i64, _i64, ctypes.POINTER(RoutingT), _vp], ctypes.c_int),
     "moe_sort_rows": ([_vp, ctypes.c_int, ctypes.POINTER(RoutingT), ctypes.c_int, _i64, _i64, _i64, _vp, _vp],
                       ctypes.c_int),
@@ -698,6 +705,98 @@ def _matrix(t: torch.Tensor | None, what: str, dtype=None, rows: int | None = No
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     if (rows is not None and t.shape[0] < rows) or (cols is not None and t.shape[1] != cols):
         raise ValueError(f"{what}: needs at least {rows} rows of {cols}, has {tuple(t.shape)}")
+
+
+# ---------------------------------------------------------------- products with one 4-bit matrix
+@dataclass
+class Linear:
+    """Device buffers of one quantised matrix [N][K] (moe_linear_t): W4G128 (w int32 [N][K/8], scale bf16
+    [N][K/128]) or NVFP4 (w uint8 [N][K/2], scale uint8 [N][K/16], gscale fp32 [1])."""
+    fmt: int
+    w: torch.Tensor
+    scale: torch.Tensor
+    gscale: torch.Tensor | None = None
+
+    def shape(self) -> tuple[int, int]:
+        """(N, K); raises unless the buffers agree."""
+        if self.fmt not in (FMT_W4G128, FMT_NVFP4):
+            raise ValueError(f"format {self.fmt} has no single-matrix product")
+        w4 = self.fmt == FMT_W4G128
+        _matrix(self.w, "w")
+        if self.w.dtype not in ((torch.int32, torch.uint32) if w4 else (torch.uint8,)):
+            raise TypeError(f"w: got {self.w.dtype}")
+        if self.scale.dtype != (torch.bfloat16 if w4 else torch.uint8):
+            raise TypeError(f"scale: got {self.scale.dtype}")
+        N, words = self.w.shape
+        K = words * (8 if w4 else 2)
+        if tuple(self.scale.shape) != (N, K // (128 if w4 else 16)):
+            raise ValueError(f"scale: expected {(N, K // (128 if w4 else 16))}, has {tuple(self.scale.shape)}")
+        if not w4:
+            if self.gscale is None:
+                raise ValueError("an NVFP4 matrix needs its per-tensor scale")
+            _check(self.gscale, "gscale", torch.float32, 1)
+        return N, K
+
+
+def quantize_linear(fmt: int, w: torch.Tensor, stream=None) -> Linear:
+    """Quantise one bf16 matrix [N][K] into W4G128 or NVFP4."""
+    _matrix(w, "w", torch.bfloat16)
+    if fmt == FMT_W4G128:
+        q, s = moe_quantize_w4g128(w[None], stream=stream)
+        return Linear(fmt, q[0], s[0])
+    if fmt == FMT_NVFP4:
+        q, s, g = moe_quantize_nvfp4(w[None], stream=stream)
+        return Linear(fmt, q[0], s[0], g)
+    raise ValueError(fmt)
+
+
+def _rows_of(t: torch.Tensor, what: str) -> int:
+    """Row distance of a 2-d tensor with adjacent elements (one row: its length)."""
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be adjacent")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def moe_linear_w4(x: torch.Tensor, w: Linear, act: int = ACT_NONE, residual: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """act(x w^T) + residual for x [T][K] (bf16 or fp16; rows may be strided): [T][N], or [T][N/2] with
+    ACT_SWIGLU, in out_dtype (default x's).  residual: [T][M] or one row [M] for all tokens."""
+    _matrix(x, "x")
+    T, K = x.shape
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"x: expected bf16 or fp16, got {x.dtype}")
+    N, wk = w.shape()
+    if wk != K:
+        raise ValueError(f"x: rows of {K}, the matrix has {wk} columns")
+    M = N // 2 if act == ACT_SWIGLU else N
+    dt = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+    if dt not in DTYPES:
+        raise TypeError(f"out: expected bf16, fp16 or fp32, got {dt}")
+    ldr = 0
+    if residual is not None:
+        if residual.dtype != dt:
+            raise TypeError(f"residual: expected {dt}, got {residual.dtype}")
+        if residual.dim() == 1:
+            if residual.shape[0] != M or (M > 1 and residual.stride(0) != 1):
+                raise ValueError(f"residual: expected {M} adjacent elements, has {tuple(residual.shape)}")
+        else:
+            if residual.dim() != 2 or tuple(residual.shape) != (T, M):
+                raise ValueError(f"residual: expected {(T, M)}, has {tuple(residual.shape)}")
+            ldr = _rows_of(residual, "residual")
+    if out is not None and tuple(out.shape) != (T, M):
+        raise ValueError(f"out: expected {(T, M)}, has {tuple(out.shape)}")
+    ldx = _rows_of(x, "x")
+    ldy = M if out is None else _rows_of(out, "out")
+    if T > 1 and ldy < M:
+        raise ValueError("out: its rows overlap")
+    dev = _device_of(x, w.w, w.scale, w.gscale, residual, out)
+    y = _new((T, M), dt, dev, stream) if out is None else out
+    wc = LinearT(w.fmt, _p(w.w), _p(w.scale), _p(w.gscale))
+    _call_on(dev, stream, "moe_linear_w4", x.data_ptr(), ldx, DTYPES[x.dtype], ctypes.byref(wc), T, N, K, act,
+             None if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, DTYPES[dt])
+    return y
 
 
 def _pairs(routing: Routing, T: int, k: int, weighted: bool) -> RoutingT:

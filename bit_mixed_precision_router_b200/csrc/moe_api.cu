@@ -414,6 +414,29 @@ static bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintpt
 static size_t dtype_size(moe_dtype_t dt) { return dt == MOE_F32 ? 4 : 2; }
 static bool dtype_ok(moe_dtype_t dt) { return dt == MOE_BF16 || dt == MOE_F16 || dt == MOE_F32; }
 
+moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, const moe_linear_t* w, int64_t T, int64_t N,
+                           int64_t K, moe_act_t act, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                           moe_dtype_t y_dtype, moe_stream_t stream) {
+  if (!w || (x_dtype != MOE_BF16 && x_dtype != MOE_F16) || !dtype_ok(y_dtype) || T < 0 || N < 1 || K < 1)
+    return MOE_ERR_INVALID_ARG;
+  if (w->fmt != MOE_FMT_W4G128 && w->fmt != MOE_FMT_NVFP4) return MOE_ERR_INVALID_ARG;
+  if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+  if (K % 128 != 0 || K > (1 << 20) || N > (1 << 30) || (act == MOE_ACT_SWIGLU && N % 2 != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T > 65535 * 64) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const int64_t M = act == MOE_ACT_SWIGLU ? N / 2 : N;
+  const int64_t most = int64_t(1) << 40;  // no row offset leaves 64 bits
+  if (ldx < K || ldx > most || ldy < M || ldy > most || (residual && ((ldr != 0 && ldr < M) || ldr > most)))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;  // no tokens; no pointer is read
+  if (!x || !y || !w->w || !w->scale || (w->fmt == MOE_FMT_NVFP4 && !w->gscale)) return MOE_ERR_INVALID_ARG;
+  const size_t ys = dtype_size(y_dtype);
+  if (!aligned16(x) || ldx % 8 != 0 || !aligned16(w->w) || !aligned16(w->scale) || !aligned_to(w->gscale, 4) ||
+      !aligned_to(y, ys) || !aligned_to(residual, ys))
+    return MOE_ERR_MISALIGNED;
+  return from_cuda(moe::launch_linear_w4(*w, x, ldx, x_dtype, int(T), int(N), int(K), act, residual, ldr, y, ldy, y_dtype,
+                                         as_stream(stream)));
+}
+
 // check_route_shape without k <= E: with dropped pairs a token may choose experts of other ranks
 static moe_status_t check_pairs_shape(int64_t T, int64_t E, int64_t k) {
   if (T < 0) return MOE_ERR_INVALID_ARG;

@@ -90,6 +90,11 @@ cudaError_t launch_gather_rows_by(const uint16_t* src, const int32_t* idx, int n
                                   cudaStream_t st);
 cudaError_t launch_ids_from_counts(const int32_t* counts, int S, int El, int32_t* ids, cudaStream_t st);
 
+// Matrix-vector products with 4-bit weights (moe_linear.cu).
+cudaError_t launch_linear_w4(const moe_linear_t& w, const void* x, int64_t ldx, moe_dtype_t x_dtype, int T, int N, int K,
+                             moe_act_t act, const void* residual, int64_t ldr, void* y, int64_t ldy, moe_dtype_t y_dtype,
+                             cudaStream_t st);
+
 // Rows sorted by expert and back (moe_rows.cu).  a: token rows [T][H]; out and b: see each call;
 // w: fp32 [T*k] or NULL (weight 1); p2r: row of each pair, negative where it has none; dw: fp32 [T*k]
 // or NULL (no dot products).

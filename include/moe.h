@@ -433,6 +433,40 @@ moe_status_t moe_combine(const uint16_t* y_rows, const moe_routing_t* routing,
                          const uint16_t* residual, int64_t T, int64_t H, int64_t k,
                          uint16_t* out, moe_stream_t stream);
 
+/* Element types of the operators below. */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype_t;
+
+/* ------------------------------------------------------------------------
+ * Matrix-vector products with 4-bit weights and group scales: the layer's dense neighbours (shared
+ * experts, projections, output heads) in the experts' formats
+ * ------------------------------------------------------------------------ */
+
+/* One quantised matrix [N][K], as moe_quantize_w4g128 or moe_quantize_nvfp4 write it with E = 1. */
+typedef struct {
+  moe_format_t fmt;    /* MOE_FMT_W4G128 or MOE_FMT_NVFP4 */
+  const void* w;       /* uint32 [N][K/8] or uint8 [N][K/2] */
+  const void* scale;   /* bf16 [N][K/128] or E4M3 uint8 [N][K/16] */
+  const float* gscale; /* NVFP4: fp32 [1], 4-byte aligned; else NULL */
+} moe_linear_t;
+
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SWIGLU = 1 /* rows 0..N/2-1 gate, N/2..N-1 up: silu(gate) * up */
+} moe_act_t;
+
+/* y[t][n] = act(sum_k x[t][k] w[n][k]) + residual[t][n], for t < T and n < M (M = N, or N/2 with
+ * SwiGLU).  No weight is rounded (W4: the group's fp32 sum is scaled; NVFP4: code times block scale is
+ * exact in 16 bits), sums in fp32 in an order fixed by T, N and K, one rounding at the end.
+ *   x bf16 or fp16, row t at x + t * ldx;  residual (NULL: none) and y of y_dtype, rows ldr and ldy
+ *   elements apart; ldr = 0: one row for all tokens (a bias).  y may be residual (with ldy = ldr).
+ * Requires K % 128 == 0, 1 <= N <= 2^30, K <= 2^20, N even with SwiGLU, ldx >= K and
+ * ldx % 8 == 0, ldy >= M, ldr = 0 or >= M; x, w, scale 16-byte aligned, y and residual aligned to their
+ * element.  Any T >= 0; the weights are read once per 64 tokens: made for decode batches (larger
+ * batches of whole experts are moe_grouped_ffn's, which takes E = 1). */
+moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, const moe_linear_t* w, int64_t T, int64_t N,
+                           int64_t K, moe_act_t act, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                           moe_dtype_t y_dtype, moe_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Tokens sorted by expert and back, with routing weights, and the gradients
  *
@@ -445,9 +479,6 @@ moe_status_t moe_combine(const uint16_t* y_rows, const moe_routing_t* routing,
  * left as they are.  1 <= H <= 2^20, 1 <= k <= MOE_MAX_TOPK.  Outputs must not overlap inputs,
  * except that out may be residual.  Deterministic.
  * ------------------------------------------------------------------------ */
-
-/* Element types of the operators below. */
-typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype_t;
 
 /* moe_permute with dropped pairs.  A pair is dropped if its id is outside 0..E-1 (padding, or an
  * expert of another rank), or if `capacity` > 0 and `capacity` pairs of smaller index have the

@@ -203,3 +203,68 @@ def test_binding_norms():
         moe.moe_block_norm(x, x, w_next=w)
     with pytest.raises(ValueError, match="dz or dh"):
         moe.moe_block_norm_bwd(x.cuda() if torch.cuda.is_available() else x, y=None)
+
+
+def test_linear(lib):
+    w = moe.LinearT(0, A, A, None)
+
+    def call(x=A, ldx=256, xt=BF16, T=4, N=32, K=256, act=0, res=None, ldr=0, y=A, ldy=32, yt=BF16):
+        return lib.moe_linear_w4(x, ldx, xt, ctypes.byref(w), T, N, K, act, res, ldr, y, ldy, yt, None)
+
+    assert call(xt=F32) == INVALID
+    assert call(yt=3) == INVALID
+    assert call(act=2) == INVALID
+    assert call(T=-1) == INVALID
+    assert call(N=0) == INVALID
+    assert call(K=200, ldx=200) == SHAPE
+    assert call(K=(1 << 20) + 128, ldx=1 << 21) == SHAPE
+    assert call(N=(1 << 30) + 1, ldy=1 << 31) == SHAPE
+    assert call(N=31, act=1) == SHAPE
+    assert call(T=65535 * 64 + 1) == SHAPE
+    assert call(ldx=248) == INVALID
+    assert call(ldx=260) == MISALIGNED
+    assert call(ldy=31) == INVALID
+    assert call(res=A, ldr=31) == INVALID
+    assert call(res=A + 1, ldr=32) == MISALIGNED
+    assert call(x=A + 8) == MISALIGNED
+    assert call(y=A + 2, yt=F32) == MISALIGNED
+    assert call(x=None) == INVALID
+    assert call(T=0, x=None) == OK
+    w.fmt = 1
+    assert call() == INVALID
+    w.fmt = 2
+    assert call() == INVALID  # NVFP4 without its per-tensor scale
+    w.scale = A + 8
+    w.gscale = A
+    assert call() == MISALIGNED
+
+
+def test_binding_linear():
+    w4 = moe.Linear(moe.FMT_W4G128, torch.zeros((32, 32), dtype=torch.int32), torch.zeros((32, 2), dtype=torch.bfloat16))
+    x = torch.zeros((4, 256), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="columns"):
+        moe.moe_linear_w4(x[:, :128], w4)
+    with pytest.raises(TypeError, match="x"):
+        moe.moe_linear_w4(x.float(), w4)
+    with pytest.raises(ValueError, match="scale"):
+        moe.moe_linear_w4(x, moe.Linear(0, w4.w, w4.scale[:, :1]))
+    with pytest.raises(TypeError, match="w:"):
+        moe.moe_linear_w4(x, moe.Linear(2, w4.w, w4.scale))
+    with pytest.raises(ValueError, match="per-tensor"):
+        moe.moe_linear_w4(x, moe.Linear(2, torch.zeros((32, 128), dtype=torch.uint8), torch.zeros((32, 16), dtype=torch.uint8)))
+    with pytest.raises(ValueError, match="format"):
+        moe.moe_linear_w4(x, moe.Linear(1, w4.w, w4.scale))
+    with pytest.raises(ValueError, match="residual"):
+        moe.moe_linear_w4(x, w4, residual=torch.zeros((4, 31), dtype=torch.bfloat16))
+    with pytest.raises(TypeError, match="residual"):
+        moe.moe_linear_w4(x, w4, residual=torch.zeros((4, 32)))
+    with pytest.raises(ValueError, match="out"):
+        moe.moe_linear_w4(x, w4, act=moe.ACT_SWIGLU, out=torch.zeros((4, 32), dtype=torch.bfloat16))
+    with pytest.raises(TypeError, match="out"):
+        moe.moe_linear_w4(x, w4, out_dtype=torch.float64)
+    with pytest.raises(ValueError, match="adjacent"):
+        moe.moe_linear_w4(torch.zeros((256, 4), dtype=torch.bfloat16).t(), w4)
+    with pytest.raises(ValueError, match="overlap"):
+        moe.moe_linear_w4(x, w4, out=torch.zeros((1, 32), dtype=torch.bfloat16).expand(4, 32))
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.moe_linear_w4(x, w4)
