@@ -655,38 +655,43 @@ def moe_combine(y_rows: torch.Tensor, routing: Routing, T: int, k: int, residual
 
 
 # ---------------------------------------------------------------- sorted by expert and back, with gradients
-def _device_of(*tensors) -> torch.device:
-    """The one CUDA device of the given tensors (None skipped)."""
-    dev = None
+def _device_of(*tensors) -> int:
+    """Index of the one CUDA device of the given tensors (None skipped)."""
+    dev = -1
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("expected a CUDA tensor")
+                if dev >= 0:
+                    raise ValueError(f"tensors on different devices: {dev} and {d}")
+                dev = d
     return dev
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """An output that belongs to the stream the call runs on."""
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """An output on the device of `like` that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _call_on(device: torch.device, stream, name: str, *args) -> None:
+def _call_on(device: int, stream, name: str, *args) -> None:
     """_call with the tensors' device current, on `stream` or that device's current stream."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream of {stream.device} with tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        _call(name, *args, _stream(stream))
+    if stream is None:
+        # the raw handle: building a torch.cuda.Stream costs as much as the launch
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        if stream.device.index != device:
+            raise ValueError(f"stream of {stream.device} with tensors on device {device}")
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device:
+        _call(name, *args, raw)
     else:
         with torch.cuda.device(device):
-            _call(name, *args, _stream(stream))
+            _call(name, *args, raw)
 
 
 def _dtype_code(t: torch.Tensor, what: str) -> int:
@@ -695,16 +700,17 @@ def _dtype_code(t: torch.Tensor, what: str) -> int:
     return DTYPES[t.dtype]
 
 
-def _matrix(t: torch.Tensor | None, what: str, dtype=None, rows: int | None = None, cols: int | None = None) -> None:
+def _matrix(t: torch.Tensor | None, what: str, dtype=None, rows: int = 0, cols: int | None = None) -> None:
     """A 2-d tensor of at least `rows` rows of `cols` elements."""
     if t is None:
         return
-    if t.dim() != 2:
-        raise ValueError(f"{what}: expected 2 dimensions, got {t.dim()}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: expected 2 dimensions, got {len(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if (rows is not None and t.shape[0] < rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{what}: needs at least {rows} rows of {cols}, has {tuple(t.shape)}")
+    if shape[0] < rows or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{what}: needs at least {rows} rows of {cols}, has {tuple(shape)}")
 
 
 # ---------------------------------------------------------------- products with one 4-bit matrix
@@ -729,7 +735,7 @@ class Linear:
             raise TypeError(f"scale: got {self.scale.dtype}")
         N, words = self.w.shape
         K = words * (8 if w4 else 2)
-        if tuple(self.scale.shape) != (N, K // (128 if w4 else 16)):
+        if self.scale.shape != (N, K // (128 if w4 else 16)):
             raise ValueError(f"scale: expected {(N, K // (128 if w4 else 16))}, has {tuple(self.scale.shape)}")
         if not w4:
             if self.gscale is None:
@@ -752,9 +758,11 @@ def quantize_linear(fmt: int, w: torch.Tensor, stream=None) -> Linear:
 
 def _rows_of(t: torch.Tensor, what: str) -> int:
     """Row distance of a 2-d tensor with adjacent elements (one row: its length)."""
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    between, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{what}: the elements of a row must be adjacent")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return between if rows > 1 else cols
 
 
 def moe_linear_w4(x: torch.Tensor, w: Linear, act: int = ACT_NONE, residual: torch.Tensor | None = None,
@@ -792,7 +800,7 @@ def moe_linear_w4(x: torch.Tensor, w: Linear, act: int = ACT_NONE, residual: tor
     if T > 1 and ldy < M:
         raise ValueError("out: its rows overlap")
     dev = _device_of(x, w.w, w.scale, w.gscale, residual, out)
-    y = _new((T, M), dt, dev, stream) if out is None else out
+    y = _new(x, (T, M), dt, stream) if out is None else out
     wc = LinearT(w.fmt, _p(w.w), _p(w.scale), _p(w.gscale))
     _call_on(dev, stream, "moe_linear_w4", x.data_ptr(), ldx, DTYPES[x.dtype], ctypes.byref(wc), T, N, K, act,
              None if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, DTYPES[dt])
@@ -818,7 +826,7 @@ def moe_permute_capacity(ids: torch.Tensor, T: int, k: int, E: int, capacity: in
     dev = _device_of(ids)
     if out is None:
         P = max(T * k, 1)
-        i32 = [_new(n, torch.int32, dev, stream) for n in (E + 1, P, P, E + 1)]
+        i32 = [_new(ids, n, torch.int32, stream) for n in (E + 1, P, P, E + 1)]
         out = Routing(ids, None, *i32)
     else:
         _check(out.sorted_pair, "sorted_pair", torch.int32, T * k)
@@ -841,7 +849,7 @@ def moe_sort_rows(x: torch.Tensor, routing: Routing, k: int, weighted: bool = Fa
     _matrix(rows, "rows", x.dtype, T * k, H)
     rc = _pairs(routing, T, k, weighted)
     dev = _device_of(x, rows, routing.pair_to_row, routing.topk_w if weighted else None)
-    rows = _new((max(T * k, 1), H), x.dtype, dev, stream) if rows is None else rows
+    rows = _new(x, (max(T * k, 1), H), x.dtype, stream) if rows is None else rows
     _call_on(dev, stream, "moe_sort_rows", _p(x), code, ctypes.byref(rc), int(weighted), T, H, k, _p(rows))
     return rows
 
@@ -865,7 +873,7 @@ def moe_unsort_rows(rows: torch.Tensor, routing: Routing, T: int, k: int, weight
     _matrix(out, "out", rows.dtype, T, H)
     rc = _pairs(routing, T, k, weighted)
     dev = _device_of(rows, residual, out, routing.pair_to_row, routing.topk_w if weighted else None)
-    out = _new((T, H), rows.dtype, dev, stream) if out is None else out
+    out = _new(rows, (T, H), rows.dtype, stream) if out is None else out
     _call_on(dev, stream, "moe_unsort_rows", _p(rows), code, ctypes.byref(rc), int(weighted), _p(residual), T, H, k,
              _p(out))
     return out
@@ -893,9 +901,10 @@ def _rows_bwd(name, a, routing, T, H, k, other, other_name, other_rows, weighted
     _check(dw, "dw", torch.float32, T * k)
     rc = _pairs(routing, T, k, weighted)
     dev = _device_of(a, other, out, dw, routing.pair_to_row, routing.topk_w if weighted else None)
-    out = _new((max(out_rows, 1) if out_name == "d_rows" else T, H), a.dtype, dev, stream) if out is None else out
+    if out is None:
+        out = _new(a, (max(out_rows, 1) if out_name == "d_rows" else T, H), a.dtype, stream)
     if dw is None and other is not None:
-        dw = _new((T * k,), torch.float32, dev, stream)
+        dw = _new(a, T * k, torch.float32, stream)
     _call_on(dev, stream, name, _p(a), code, ctypes.byref(rc), int(weighted), _p(other), T, H, k, _p(out), _p(dw))
     return out, dw
 
@@ -908,7 +917,7 @@ def moe_route_topk_bwd(dw: torch.Tensor, routing: Routing, T: int, E: int, k: in
     _check(routing.topk_w, "topk_w", torch.float32, T * k)
     _matrix(d_logits, "d_logits", torch.float32, T, E)
     dev = _device_of(dw, routing.topk_ids, routing.topk_w, d_logits)
-    d_logits = _new((T, E), torch.float32, dev, stream) if d_logits is None else d_logits
+    d_logits = _new(dw, (T, E), torch.float32, stream) if d_logits is None else d_logits
     rc = RoutingT(_p(routing.topk_ids), _p(routing.topk_w), None, None, None, None)
     _call_on(dev, stream, "moe_route_topk_bwd", _p(dw), ctypes.byref(rc), T, E, k, _p(d_logits))
     return d_logits
@@ -960,9 +969,9 @@ def moe_block_norm(x: torch.Tensor, y: torch.Tensor | None = None, routing: Rout
     _matrix(h, "h", x.dtype, T, H)
     _device_of(x, z, h)
     if z is None and y is not None:
-        z = _new((T, H), x.dtype, dev, stream)
+        z = _new(x, (T, H), x.dtype, stream)
     if h is None and w_next is not None:
-        h = _new((T, H), x.dtype, dev, stream)
+        h = _new(x, (T, H), x.dtype, stream)
     _call_on(dev, stream, "moe_block_norm", ctypes.byref(step), _p(x), code, T, H, _p(z), _p(h))
     return z, h
 
@@ -997,17 +1006,17 @@ def moe_block_norm_bwd(z: torch.Tensor, dz: torch.Tensor | None = None, dh: torc
     _matrix(dh, "dh", z.dtype, T, H)
     _device_of(z, dz, dh, workspace)
     f32 = torch.float32
-    g = BlockNormGrads(_new((T, H), z.dtype, dev, stream))
+    g = BlockNormGrads(_new(z, (T, H), z.dtype, stream))
     if y is not None:
-        g.dy = _new((T, H), z.dtype, dev, stream)
+        g.dy = _new(z, (T, H), z.dtype, stream)
     if gate is not None:
-        g.dgate = _new((T,) if gate.dim() == 1 else (T, H), gate.dtype, dev, stream)
+        g.dgate = _new(z, T if gate.dim() == 1 else (T, H), gate.dtype, stream)
     if w_post is not None:
-        g.dw_post = _new((H,), f32, dev, stream)
+        g.dw_post = _new(z, H, f32, stream)
     if dh is not None:
-        g.dw_next = _new((H,), f32, dev, stream)
+        g.dw_next = _new(z, H, f32, stream)
     if workspace is None:
-        workspace = _new((max(moe_block_norm_bwd_workspace_bytes(T, H), 16),), torch.uint8, dev, stream)
+        workspace = _new(z, max(moe_block_norm_bwd_workspace_bytes(T, H), 16), torch.uint8, stream)
     gc = BlockNormGradsT(_p(g.dx), _p(g.dy), _p(g.dgate), _p(g.dw_post), _p(g.dw_next))
     _call_on(dev, stream, "moe_block_norm_bwd", ctypes.byref(step), _p(z), _p(dz), _p(dh), code, T, H, ctypes.byref(gc),
              _p(workspace), workspace.numel() * workspace.element_size())

@@ -13,6 +13,9 @@
 // A persistent grid: each CTA walks rows t = b, b + gridDim.x, ... with its columns fixed per
 // thread, so the weight gradients accumulate in registers (fp32) and each CTA writes one partial row;
 // a second kernel adds the partial rows in CTA order (no atomics: the result does not depend on timing).
+#include <atomic>
+#include <climits>
+
 #include "moe_internal.h"
 #include "moe_vec.cuh"
 
@@ -33,6 +36,8 @@ struct NormArgs {
   float *dgate_tok, *part;
 };
 
+constexpr int kNormSlots = 8;  // routed rows in flight per thread
+
 MOE_DEVICE float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
 
 // The sigmoid and its derivative without the cancellation of a (1 - a): with e = exp(-|v|) <= 1,
@@ -43,45 +48,67 @@ MOE_DEVICE void sigmoid_grad(const float v, float& a, float& da) {
   da = e * s * s;
 }
 
-// W: vectors of V elements per thread.
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(1024) k_block_norm(NormArgs a) {
+// W: vectors of V elements per thread.  The row's loads are all issued before the first sum.  ROUTED: y is the
+// weighted sum of the token's routed rows.
+template <typename T, int V, int W, int THREADS, int CTAS, bool ROUTED>
+__global__ void __launch_bounds__(THREADS, CTAS) k_block_norm(NormArgs a) {
   __shared__ float red[2][32];
   const int t = blockIdx.x, nv = a.H / V;
   const size_t off = size_t(t) * a.H;
-  const T* x = static_cast<const T*>(a.x) + off;
-  float z[W][V];
-  float inv_h = 1.0f / float(a.H);
+  const float inv_h = 1.0f / float(a.H);
+  Pack<T, V> xp[W], gp[W];
+  float y[W][V];
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
+    xp[i] = Pack<T, V>::zero();
     if (v < nv) {
-      load_vec<T, V>(x, v).unpack(z[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) z[i][e] = 0.0f;
+      xp[i] = load_vec<T, V>(static_cast<const T*>(a.x) + off, v);
+      if (a.gate_full) gp[i] = load_vec_once<T, V>(static_cast<const T*>(a.gate_full) + off, v);
     }
   }
   if (a.y) {
-    float y[W][V];
+    if (!ROUTED) {
+      Pack<T, V> yp[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
+      for (int i = 0; i < W; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        yp[i] = Pack<T, V>::zero();
+        if (v < nv) yp[i] = load_vec_once<T, V>(static_cast<const T*>(a.y) + off, v);
+      }
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[i][e] = 0.0f;
-      if (v >= nv) continue;
-      if (!a.p2r) {
-        load_vec_once<T, V>(static_cast<const T*>(a.y) + off, v).unpack(y[i]);
-      } else {
-#pragma unroll 8
-        for (int j = 0; j < a.k; ++j) {
-          const int row = a.p2r[size_t(t) * a.k + j];
-          const float w = a.topk_w ? a.topk_w[size_t(t) * a.k + j] : 1.0f;
-          if (row < 0) continue;
-          float f[V];
-          load_vec_once<T, V>(static_cast<const T*>(a.y) + size_t(row) * a.H, v).unpack(f);
+      for (int i = 0; i < W; ++i) yp[i].unpack(y[i]);
+    } else {
 #pragma unroll
-          for (int e = 0; e < V; ++e) y[i][e] = fmaf(w, f[e], y[i][e]);
+      for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[i][e] = 0.0f;
+      // the token's rows, kNormSlots at a time, in slot order
+      for (int j0 = 0; j0 < a.k; j0 += kNormSlots) {
+        int row[kNormSlots];
+        float w[kNormSlots];
+#pragma unroll
+        for (int j = 0; j < kNormSlots; ++j) {
+          const size_t p = size_t(t) * a.k + j0 + j;
+          row[j] = j0 + j < a.k ? a.p2r[p] : -1;
+          w[j] = a.topk_w && j0 + j < a.k ? a.topk_w[p] : 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const int v = threadIdx.x + i * blockDim.x;
+          if (v >= nv) continue;
+          Pack<T, V> r[kNormSlots];
+#pragma unroll
+          for (int j = 0; j < kNormSlots; ++j)
+            if (row[j] >= 0) r[j] = load_vec_once<T, V>(static_cast<const T*>(a.y) + size_t(row[j]) * a.H, v);
+#pragma unroll
+          for (int j = 0; j < kNormSlots; ++j) {
+            if (row[j] < 0) continue;
+            float f[V];
+            r[j].unpack(f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[i][e] = fmaf(w[j], f[e], y[i][e]);
+          }
         }
       }
     }
@@ -99,33 +126,36 @@ __global__ void __launch_bounds__(1024) k_block_norm(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nv) continue;
-      float m[V];
+      float m[V], xf[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) m[e] = scale;
-      if (a.w_post) {
+      if (a.w_post && v < nv) {
         float w[V];
         load_vec<T, V>(static_cast<const T*>(a.w_post), v).unpack(w);
 #pragma unroll
         for (int e = 0; e < V; ++e) m[e] *= w[e];
       }
-      if (a.gate_full) {
+      if (a.gate_full && v < nv) {
         float g[V];
-        load_vec_once<T, V>(static_cast<const T*>(a.gate_full) + off, v).unpack(g);
+        gp[i].unpack(g);
 #pragma unroll
         for (int e = 0; e < V; ++e) m[e] *= a.sigmoid ? sigmoid(g[e]) : g[e];
       }
+      xp[i].unpack(xf);
 #pragma unroll
-      for (int e = 0; e < V; ++e) z[i][e] = fmaf(m[e], y[i][e], z[i][e]);
-      store_vec(static_cast<T*>(a.z) + off, v, Pack<T, V>::of(z[i]));
+      for (int e = 0; e < V; ++e) y[i][e] = fmaf(m[e], y[i][e], xf[e]);  // z; zeros past the row's end
+      if (v < nv) store_vec(static_cast<T*>(a.z) + off, v, Pack<T, V>::of(y[i]));
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) xp[i].unpack(y[i]);
   }
   if (!a.h) return;
   float s[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < W; ++i)
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[0] = fmaf(z[i][e], z[i][e], s[0]);
+    for (int e = 0; e < V; ++e) s[0] = fmaf(y[i][e], y[i][e], s[0]);
   block_sum<1>(s, red[1]);
   const float r = rsqrtf(s[0] * inv_h + a.eps);
 #pragma unroll
@@ -135,46 +165,94 @@ __global__ void __launch_bounds__(1024) k_block_norm(NormArgs a) {
     float w[V];
     load_vec<T, V>(static_cast<const T*>(a.w_next), v).unpack(w);
 #pragma unroll
-    for (int e = 0; e < V; ++e) w[e] *= z[i][e] * r;
+    for (int e = 0; e < V; ++e) w[e] *= y[i][e] * r;
     store_vec(static_cast<T*>(a.h) + off, v, Pack<T, V>::of(w));
   }
 }
 
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(1024) k_block_norm_bwd(NormArgs a) {
+// The rows of the backward pass wait in shared memory: every thread copies its own vectors of the next rows
+// (cp.async, no barrier: it reads back what it copied itself) while it works on the current one.
+template <typename T, int V>
+MOE_DEVICE void copy_vec(Pack<T, V>* dst, const T* row, int v) {
+  if constexpr (sizeof(Pack<T, V>) == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(row + size_t(v) * V) : "memory");
+  else
+    *dst = load_vec<T, V>(row, v);
+}
+
+enum { kZ, kDh, kDz, kY, kGate, kArrays };  // arrays of a stage
+
+// DIRECT: rows too long for a stage are read from global memory (the second reading from L2).
+template <typename T, int V, int W, int THREADS, bool DIRECT>
+__global__ void __launch_bounds__(THREADS) k_block_norm_bwd(NormArgs a, int depth) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red1[3 * 32], red2[32];
-  const int nv = a.H / V;
+  const int nv = a.H / V, nth = blockDim.x, arrays = a.gate_full ? kArrays : kArrays - 1;
   const float inv_h = 1.0f / float(a.H);
+  auto slot = [&](int stage, int arr, int i) {
+    return reinterpret_cast<Pack<T, V>*>(smem) + ((stage * arrays + arr) * W + i) * nth + threadIdx.x;
+  };
+  auto get = [&](int stage, int arr, int i, size_t off) {
+    if constexpr (DIRECT) {
+      const void* const from[kArrays] = {a.x, a.dh, a.dz, a.y, a.gate_full};
+      return load_vec<T, V>(static_cast<const T*>(from[arr]) + off, threadIdx.x + i * nth);
+    } else {
+      return *slot(stage, arr, i);
+    }
+  };
+  auto fetch = [&](int t, int stage) {
+    if (DIRECT) return;
+    if (t < a.T) {
+      const size_t off = size_t(t) * a.H;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const int v = threadIdx.x + i * nth;
+        if (v >= nv) continue;
+        if (a.dh) {
+          copy_vec(slot(stage, kZ, i), static_cast<const T*>(a.x) + off, v);
+          copy_vec(slot(stage, kDh, i), static_cast<const T*>(a.dh) + off, v);
+        }
+        if (a.dz) copy_vec(slot(stage, kDz, i), static_cast<const T*>(a.dz) + off, v);
+        if (a.y) copy_vec(slot(stage, kY, i), static_cast<const T*>(a.y) + off, v);
+        if (a.gate_full) copy_vec(slot(stage, kGate, i), static_cast<const T*>(a.gate_full) + off, v);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  Pack<T, V> wn[W], wp[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const int v = threadIdx.x + i * nth;
+    wn[i] = wp[i] = Pack<T, V>::zero();
+    if (v < nv && a.dh) wn[i] = load_vec<T, V>(static_cast<const T*>(a.w_next), v);
+    if (v < nv && a.w_post) wp[i] = load_vec<T, V>(static_cast<const T*>(a.w_post), v);
+  }
   float gp[W][V], gn[W][V];  // this CTA's sums for dw_post, dw_next
 #pragma unroll
   for (int i = 0; i < W; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) gp[i][e] = gn[i][e] = 0.0f;
+  for (int s = 0; s + 1 < depth; ++s) fetch(blockIdx.x + s * gridDim.x, s);
+  int stage = 0;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    // the stage of the row before this one is free: its reads were the thread's own
+    fetch(t + (depth - 1) * gridDim.x, stage == 0 ? depth - 1 : stage - 1);
+    if (depth == 3)
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (depth == 2)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     const size_t off = size_t(t) * a.H;
-    Pack<T, V> z[W], y[W], dz[W], dh[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      z[i] = y[i] = dz[i] = dh[i] = Pack<T, V>::zero();
-      if (v >= nv) continue;
-      if (a.dh) {
-        z[i] = load_vec<T, V>(static_cast<const T*>(a.x) + off, v);
-        dh[i] = load_vec<T, V>(static_cast<const T*>(a.dh) + off, v);
-      }
-      if (a.dz) dz[i] = load_vec<T, V>(static_cast<const T*>(a.dz) + off, v);
-      if (a.y) y[i] = load_vec<T, V>(static_cast<const T*>(a.y) + off, v);
-    }
     float s[3] = {0.0f, 0.0f, 0.0f};  // <z, z>, <z, w_next dh>, <y, y>
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nv) continue;
+      if (threadIdx.x + i * nth >= nv) continue;
       float zf[V], f[V], w[V];
       if (a.dh) {
-        z[i].unpack(zf);
-        dh[i].unpack(f);
-        load_vec<T, V>(static_cast<const T*>(a.w_next), v).unpack(w);
+        get(stage, kZ, i, off).unpack(zf);
+        get(stage, kDh, i, off).unpack(f);
+        wn[i].unpack(w);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           s[0] = fmaf(zf[e], zf[e], s[0]);
@@ -182,7 +260,7 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(NormArgs a) {
         }
       }
       if (a.w_post) {
-        y[i].unpack(f);
+        get(stage, kY, i, off).unpack(f);
 #pragma unroll
         for (int e = 0; e < V; ++e) s[2] = fmaf(f[e], f[e], s[2]);
       }
@@ -200,14 +278,19 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(NormArgs a) {
     float s2[1] = {0.0f};  // <y, w_post d> (with the elementwise gate: <y, w_post a d>)
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
+      const int v = threadIdx.x + i * nth;
       if (v >= nv) continue;
-      dz[i].unpack(d[i]);
+      if (a.dz) {
+        get(stage, kDz, i, off).unpack(d[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[i][e] = 0.0f;
+      }
       if (a.dh) {
         float zf[V], f[V], w[V];
-        z[i].unpack(zf);
-        dh[i].unpack(f);
-        load_vec<T, V>(static_cast<const T*>(a.w_next), v).unpack(w);
+        get(stage, kZ, i, off).unpack(zf);
+        get(stage, kDh, i, off).unpack(f);
+        wn[i].unpack(w);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           gn[i][e] = fmaf(f[e], zf[e] * r, gn[i][e]);
@@ -216,12 +299,12 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(NormArgs a) {
       }
       if (a.dx) store_vec(static_cast<T*>(a.dx) + off, v, Pack<T, V>::of(d[i]));
       if (!a.y) continue;
-      float yf[V], w[V], g[V];
-      y[i].unpack(yf);
-      if (a.w_post) load_vec<T, V>(static_cast<const T*>(a.w_post), v).unpack(w);
-      if (a.gate_full) load_vec<T, V>(static_cast<const T*>(a.gate_full) + off, v).unpack(g);
+      float yf[V], w[V];
+      get(stage, kY, i, off).unpack(yf);
+      wp[i].unpack(w);
       if (a.gate_full) {
-        float dg[V];
+        float g[V], dg[V];
+        get(stage, kGate, i, off).unpack(g);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float n = a.w_post ? yf[e] * q * w[e] : yf[e];
@@ -236,20 +319,19 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(NormArgs a) {
       for (int e = 0; e < V; ++e) s2[0] = fmaf(yf[e], (a.w_post ? w[e] : 1.0f) * d[i][e], s2[0]);
     }
     if (a.y) {
-      const bool sum2 = a.w_post || a.gate_tok;
-      if (sum2) block_sum<1>(s2, red2);
+      if (a.w_post || a.gate_tok) block_sum<1>(s2, red2);
       if (a.dgate_tok && threadIdx.x == 0) a.dgate_tok[t] = a.alpha * dat * q * s2[0];
       const float c = a.alpha * at;
       const float yc = q * q * (s2[0] * inv_h);  // dy = c q (w_post d - y yc)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
+        const int v = threadIdx.x + i * nth;
         if (v >= nv) continue;
         float o[V];
         if (a.w_post) {
           float yf[V], w[V];
-          y[i].unpack(yf);
-          load_vec<T, V>(static_cast<const T*>(a.w_post), v).unpack(w);
+          get(stage, kY, i, off).unpack(yf);
+          wp[i].unpack(w);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             gp[i][e] = fmaf(c * d[i][e], yf[e] * q, gp[i][e]);
@@ -262,13 +344,14 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(NormArgs a) {
         if (a.dy) store_vec(static_cast<T*>(a.dy) + off, v, Pack<T, V>::of(o));
       }
     }
-    __syncthreads();  // the next row's sums reuse red1 and red2
+    stage = stage + 1 == depth ? 0 : stage + 1;
+    if (!a.y || !(a.w_post || a.gate_tok)) __syncthreads();  // the next row's first sum reuses red1: the second sum's barrier, or this one, lies between
   }
   // partial rows: [gridDim.x][2][H]
   float* part = a.part + size_t(blockIdx.x) * 2 * a.H;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
+    const int v = threadIdx.x + i * nth;
     if (v >= nv) continue;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -295,7 +378,14 @@ __global__ void __launch_bounds__(1024) k_norm_weight_sum(const float* __restric
 }
 
 // ---------------------------------------------------------------- launchers
-constexpr int kBwdCtas = 148;  // one persistent CTA per SM: partial rows of the weight gradients
+int round32(int n) { return (n + 31) / 32 * 32; }
+
+// Persistent CTAs per SM of the backward pass: 768 threads (80 registers each), at most 8 CTAs.
+constexpr int kSms = 148;
+int bwd_per_sm(int threads) {
+  const int n = 768 / threads;
+  return n < 1 ? 1 : n > 8 ? 8 : n;
+}
 
 NormArgs args_of(const moe_block_norm_t& b, int T, int H) {
   NormArgs a = {};
@@ -315,51 +405,98 @@ NormArgs args_of(const moe_block_norm_t& b, int T, int H) {
   return a;
 }
 
-int round32(int n) { return (n + 31) / 32 * 32; }
-
-template <typename T, int V>
+template <typename T, int V, bool ROUTED>
 cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
   const int nv = a.H / V;
-  if (nv <= 1024)
-    k_block_norm<T, V, 1><<<unsigned(a.T), round32(nv), 0, st>>>(a);
+  const unsigned rows = unsigned(a.T);
+  // Few rows: a vector per thread, the shortest path through the row.  Many: two vectors per thread, so that
+  // several CTAs share an SM and one's loads run during the others' sums.
+  if (nv <= 1024 && (a.T < 2 * kSms || nv <= 64))
+    k_block_norm<T, V, 1, 1024, 1, ROUTED><<<rows, round32(nv), 0, st>>>(a);
+  else if (nv <= 1024)
+    k_block_norm<T, V, 2, 512, 2, ROUTED><<<rows, round32((nv + 1) / 2), 0, st>>>(a);
   else if (nv <= 4096)
-    k_block_norm<T, V, 4><<<unsigned(a.T), round32((nv + 3) / 4), 0, st>>>(a);
+    k_block_norm<T, V, 4, V == 8 ? 512 : 1024, 1, ROUTED><<<rows, round32((nv + 3) / 4), 0, st>>>(a);
   else if constexpr (V == 1)
-    k_block_norm<T, V, 16><<<unsigned(a.T), round32((nv + 15) / 16), 0, st>>>(a);
+    k_block_norm<T, V, 16, 1024, 1, ROUTED><<<rows, round32((nv + 15) / 16), 0, st>>>(a);
   else
     return cudaErrorInvalidValue;
+  return cudaGetLastError();
+}
+
+// Threads and vectors per thread of a backward row, and with them the grid.
+template <typename T, int V>
+int bwd_width(int H) {
+  const int nv = H / V;
+  return nv <= 1024 ? 1 : nv <= 4096 ? 4 : 16;
+}
+template <typename T, int V>
+int bwd_grid(int T_, int H) {
+  const int nv = (H + V - 1) / V, w = bwd_width<T, V>(H), grid = kSms * bwd_per_sm(round32((nv + w - 1) / w));
+  return T_ < grid ? T_ : grid;
+}
+
+// bytes of a stage: a row of every array
+template <typename T, int V>
+int bwd_stage(const NormArgs& a) {
+  const int w = bwd_width<T, V>(a.H);
+  return (a.gate_full ? kArrays : kArrays - 1) * w * round32((a.H / V + w - 1) / w) * int(sizeof(Pack<T, V>));
+}
+constexpr int kSmemMax = 224 * 1024;
+
+template <typename T, int V, int W, int THREADS, bool DIRECT>
+cudaError_t run_bwd(const NormArgs& a, cudaStream_t st) {
+  // raised once per device, so no later call (e.g. one inside a stream capture) sets attributes
+  static std::atomic<bool> done[128] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    err = cudaFuncSetAttribute(k_block_norm_bwd<T, V, W, THREADS, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (err != cudaSuccess) return err;
+    done[dev].store(true, std::memory_order_release);
+  }
+  const int threads = round32((a.H / V + W - 1) / W), stage = bwd_stage<T, V>(a);
+  const int room = kSmemMax / bwd_per_sm(threads);
+  const int depth = DIRECT ? 0 : 3 * stage <= room ? 3 : 2 * stage <= room ? 2 : 1;
+  k_block_norm_bwd<T, V, W, THREADS, DIRECT><<<unsigned(bwd_grid<T, V>(a.T, a.H)), threads, size_t(depth) * stage, st>>>(a, depth);
   return cudaGetLastError();
 }
 
 template <typename T, int V>
-cudaError_t norm_bwd(const NormArgs& a, cudaStream_t st) {
+cudaError_t norm_bwd(const NormArgs& a, int* grid, cudaStream_t st) {
+  *grid = bwd_grid<T, V>(a.T, a.H);
+  const int w = bwd_width<T, V>(a.H);
   const int nv = a.H / V;
-  const unsigned grid = unsigned(a.T < kBwdCtas ? a.T : kBwdCtas);
-  if (nv <= 1024)
-    k_block_norm_bwd<T, V, 1><<<grid, round32(nv), 0, st>>>(a);
-  else if (nv <= 4096)
-    k_block_norm_bwd<T, V, 4><<<grid, round32((nv + 3) / 4), 0, st>>>(a);
-  else if constexpr (V == 1)
-    k_block_norm_bwd<T, V, 16><<<grid, round32((nv + 15) / 16), 0, st>>>(a);
-  else
-    return cudaErrorInvalidValue;
-  return cudaGetLastError();
+  if (w == 1) {
+    if (nv <= 768) return run_bwd<T, V, 1, 768, false>(a, st);
+    return nv <= 896 ? run_bwd<T, V, 1, 896, false>(a, st) : run_bwd<T, V, 1, 1024, false>(a, st);
+  }
+  // H <= 16384: at most 512 threads of four 8-element vectors, 1024 of narrower ones
+  const bool direct = bwd_stage<T, V>(a) > kSmemMax;
+  constexpr int most = V == 8 ? 512 : 1024;
+  if (w == 4) return direct ? run_bwd<T, V, 4, most, true>(a, st) : run_bwd<T, V, 4, most, false>(a, st);
+  if constexpr (V == 1) return direct ? run_bwd<T, V, 16, 1024, true>(a, st) : run_bwd<T, V, 16, 1024, false>(a, st);
+  return cudaErrorInvalidValue;
 }
 
+// grid NULL: forward; else backward, and the number of partial rows is stored there
 template <typename T>
-cudaError_t norm_of(const NormArgs& a, bool bwd, cudaStream_t st) {
+cudaError_t norm_of(const NormArgs& a, int* grid, cudaStream_t st) {
   constexpr int V = vec_width<T>();
   bool wide = a.H % V == 0;
   const void* ps[] = {a.x, a.y, a.w_post, a.w_next, a.gate_full, a.z, a.h, a.dz, a.dh, a.dx, a.dy, a.dgate_full};
   for (const void* p : ps) wide = wide && vec_aligned(p);
-  if (bwd) return wide ? norm_bwd<T, V>(a, st) : norm_bwd<T, 1>(a, st);
-  return wide ? norm_fwd<T, V>(a, st) : norm_fwd<T, 1>(a, st);
+  if (grid) return wide ? norm_bwd<T, V>(a, grid, st) : norm_bwd<T, 1>(a, grid, st);
+  if (a.p2r) return wide ? norm_fwd<T, V, true>(a, st) : norm_fwd<T, 1, true>(a, st);
+  return wide ? norm_fwd<T, V, false>(a, st) : norm_fwd<T, 1, false>(a, st);
 }
 
-cudaError_t norm_any(const NormArgs& a, moe_dtype_t dt, bool bwd, cudaStream_t st) {
-  if (dt == MOE_BF16) return norm_of<__nv_bfloat16>(a, bwd, st);
-  if (dt == MOE_F16) return norm_of<__half>(a, bwd, st);
-  return norm_of<float>(a, bwd, st);
+cudaError_t norm_any(const NormArgs& a, moe_dtype_t dt, int* grid, cudaStream_t st) {
+  if (dt == MOE_BF16) return norm_of<__nv_bfloat16>(a, grid, st);
+  if (dt == MOE_F16) return norm_of<__half>(a, grid, st);
+  return norm_of<float>(a, grid, st);
 }
 
 }  // namespace
@@ -370,11 +507,14 @@ cudaError_t launch_block_norm(const moe_block_norm_t& b, const void* x, int T, i
   a.x = x;
   a.z = z;
   a.h = h;
-  return norm_any(a, dt, false, st);
+  return norm_any(a, dt, nullptr, st);
 }
 
+// the largest grid over the element types and alignments
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H) {
-  const int64_t g = T < kBwdCtas ? T : kBwdCtas;
+  const int t = T < INT_MAX ? int(T) : INT_MAX, h = H < 16384 ? int(H) : 16384;
+  int g = 0;
+  for (int n : {bwd_grid<__nv_bfloat16, 8>(t, h), bwd_grid<float, 4>(t, h), bwd_grid<float, 1>(t, h)}) g = n > g ? n : g;
   return size_t(g) * 2 * size_t(H) * sizeof(float);
 }
 
@@ -389,10 +529,10 @@ cudaError_t launch_block_norm_bwd(const moe_block_norm_t& b, const void* z, cons
   if (b.gate_mode == MOE_GATE_TOKEN) a.dgate_tok = static_cast<float*>(g.dgate);
   if (b.gate_mode == MOE_GATE_FULL) a.dgate_full = g.dgate;
   a.part = static_cast<float*>(ws);
-  cudaError_t err = norm_any(a, dt, true, st);
+  int grid = 0;
+  cudaError_t err = norm_any(a, dt, &grid, st);
   if (err != cudaSuccess || (!g.dw_post && !g.dw_next)) return err;
-  k_norm_weight_sum<<<dim3(unsigned((H + 31) / 32), 2), 1024, 0, st>>>(a.part, T < kBwdCtas ? T : kBwdCtas, H, g.dw_post,
-                                                                       g.dw_next);
+  k_norm_weight_sum<<<dim3(unsigned((H + 31) / 32), 2), 1024, 0, st>>>(a.part, grid, H, g.dw_post, g.dw_next);
   return cudaGetLastError();
 }
 

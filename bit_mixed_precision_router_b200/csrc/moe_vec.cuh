@@ -24,13 +24,30 @@ MOE_DEVICE float from_float<float>(float f) {
   return f;
 }
 
+MOE_DEVICE void unpack2(uint32_t w, float& lo, float& hi, __nv_bfloat16) {
+  lo = bf16_lo(w);
+  hi = bf16_hi(w);
+}
+MOE_DEVICE void unpack2(uint32_t w, float& lo, float& hi, __half) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  lo = v.x;
+  hi = v.y;
+}
+
 // V elements as they lie in memory (kept packed while a load is in flight).
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Pack {
   T e[V];
   MOE_DEVICE void unpack(float (&f)[V]) const {
+    if constexpr (V == 8) {  // two 16-bit elements per register
+      const uint4 u = *reinterpret_cast<const uint4*>(e);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = to_float(e[i]);
+      for (int i = 0; i < 4; ++i) unpack2(w[i], f[2 * i], f[2 * i + 1], T());
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = to_float(e[i]);
+    }
   }
   MOE_DEVICE static Pack of(const float (&f)[V]) {
     Pack p;
