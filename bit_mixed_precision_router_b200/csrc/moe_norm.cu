@@ -38,12 +38,13 @@ struct NormArgs {
 
 constexpr int kNormSlots = 8;  // routed rows in flight per thread
 
-MOE_DEVICE float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// __fdividef: within 2 units of the last place for denominators below 2^126, 0 above (where the quotient is below 2^-126)
+MOE_DEVICE float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
 
 // The sigmoid and its derivative without the cancellation of a (1 - a): with e = exp(-|v|) <= 1,
 // sigmoid(|v|) = 1 / (1 + e), sigmoid(-|v|) = e / (1 + e) and the derivative e / (1 + e)^2.
 MOE_DEVICE void sigmoid_grad(const float v, float& a, float& da) {
-  const float e = expf(-fabsf(v)), s = 1.0f / (1.0f + e);
+  const float e = expf(-fabsf(v)), s = __fdividef(1.0f, 1.0f + e);
   a = v >= 0.0f ? s : e * s;
   da = e * s * s;
 }
@@ -180,17 +181,29 @@ MOE_DEVICE void copy_vec(Pack<T, V>* dst, const T* row, int v) {
     *dst = load_vec<T, V>(row, v);
 }
 
+// Persistent CTAs per SM: 768 threads (80 registers each), one CTA of more.
+__host__ __device__ constexpr int bwd_ctas(int threads) { return threads > 768 ? 1 : 768 / threads; }
+
 enum { kZ, kDh, kDz, kY, kGate, kArrays };  // arrays of a stage
 
-// DIRECT: rows too long for a stage are read from global memory (the second reading from L2).
+// bytes of a stage: a row of every array
+template <typename T, int V, int W, int THREADS>
+__host__ __device__ constexpr int bwd_stage_bytes(bool gate) {
+  return (gate ? kArrays : kArrays - 1) * W * THREADS * int(sizeof(Pack<T, V>));
+}
+
+// DIRECT: rows too long for two stages are read from global memory (the second reading from L2).
 template <typename T, int V, int W, int THREADS, bool DIRECT>
-__global__ void __launch_bounds__(THREADS) k_block_norm_bwd(NormArgs a, int depth) {
+__global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(NormArgs a, int depth) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float red1[3 * 32], red2[32];
-  const int nv = a.H / V, nth = blockDim.x, arrays = a.gate_full ? kArrays : kArrays - 1;
+  __shared__ float red1[4 * 32], red2[4 * 32];
+  const int nv = a.H / V, nth = blockDim.x;
+  const int stage_bytes = bwd_stage_bytes<T, V, W, THREADS>(a.gate_full != nullptr);
   const float inv_h = 1.0f / float(a.H);
+  uint8_t* const mine = smem + threadIdx.x * sizeof(Pack<T, V>);
+  // array and vector at offsets known to the compiler: spaced for THREADS threads, whatever the launch has
   auto slot = [&](int stage, int arr, int i) {
-    return reinterpret_cast<Pack<T, V>*>(smem) + ((stage * arrays + arr) * W + i) * nth + threadIdx.x;
+    return reinterpret_cast<Pack<T, V>*>(mine + stage * stage_bytes + (arr * W + i) * THREADS * int(sizeof(Pack<T, V>)));
   };
   auto get = [&](int stage, int arr, int i, size_t off) {
     if constexpr (DIRECT) {
@@ -232,19 +245,8 @@ __global__ void __launch_bounds__(THREADS) k_block_norm_bwd(NormArgs a, int dept
   for (int i = 0; i < W; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) gp[i][e] = gn[i][e] = 0.0f;
-  for (int s = 0; s + 1 < depth; ++s) fetch(blockIdx.x + s * gridDim.x, s);
-  int stage = 0;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    // the stage of the row before this one is free: its reads were the thread's own
-    fetch(t + (depth - 1) * gridDim.x, stage == 0 ? depth - 1 : stage - 1);
-    if (depth == 3)
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (depth == 2)
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    const size_t off = size_t(t) * a.H;
-    float s[3] = {0.0f, 0.0f, 0.0f};  // <z, z>, <z, w_next dh>, <y, y>
+  // <z, z>, <z, w_next dh>, <y, y> of a row
+  auto first_sums = [&](float* s, int stage, size_t off) {
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       if (threadIdx.x + i * nth >= nv) continue;
@@ -265,17 +267,35 @@ __global__ void __launch_bounds__(THREADS) k_block_norm_bwd(NormArgs a, int dept
         for (int e = 0; e < V; ++e) s[2] = fmaf(f[e], f[e], s[2]);
       }
     }
+  };
+  float r = 0.0f, q = 1.0f, zc = 0.0f;  // d = dz + r (w dh - z zc)
+  auto statistics = [&](const float* s) {
+    if (a.dh) r = rsqrtf(s[0] * inv_h + a.eps);
+    if (a.w_post) q = rsqrtf(s[2] * inv_h + a.eps);
+    zc = r * r * (s[1] * inv_h);
+  };
+  // One barrier per row: the second sum of row t and the first sums of the CTA's next row are joined together.
+  int stage = 0, ahead = 1;
+  fetch(blockIdx.x, 0);
+  fetch(blockIdx.x + gridDim.x, 1);
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+  {
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    first_sums(s, 0, size_t(blockIdx.x) * a.H);
     block_sum<3>(s, red1);
-    const float r = a.dh ? rsqrtf(s[0] * inv_h + a.eps) : 0.0f;
-    const float q = a.w_post ? rsqrtf(s[2] * inv_h + a.eps) : 1.0f;
-    const float zc = r * r * (s[1] * inv_h);  // d = dz + r (w dh - z zc)
-    float at = 1.0f, dat = 1.0f;              // the token's gate and its derivative
+    statistics(s);
+  }
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x, ahead ^= 1) {
+    const int after = stage + 1 == depth ? 0 : stage + 1;  // the next row's stage
+    if (depth == 3) fetch(t + 2 * gridDim.x, after + 1 == depth ? 0 : after + 1);
+    const size_t off = size_t(t) * a.H;
+    float at = 1.0f, dat = 1.0f;  // the token's gate and its derivative
     if (a.gate_tok) {
       at = a.gate_tok[t];
       if (a.sigmoid) sigmoid_grad(at, at, dat);
     }
     float d[W][V];
-    float s2[1] = {0.0f};  // <y, w_post d> (with the elementwise gate: <y, w_post a d>)
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // [3]: <y, w_post d> (with the elementwise gate: <y, w_post a d>)
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       const int v = threadIdx.x + i * nth;
@@ -301,28 +321,37 @@ __global__ void __launch_bounds__(THREADS) k_block_norm_bwd(NormArgs a, int dept
       if (!a.y) continue;
       float yf[V], w[V];
       get(stage, kY, i, off).unpack(yf);
-      wp[i].unpack(w);
+      if (a.w_post) {
+        wp[i].unpack(w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[e] = 1.0f;
+      }
       if (a.gate_full) {
         float g[V], dg[V];
         get(stage, kGate, i, off).unpack(g);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float n = a.w_post ? yf[e] * q * w[e] : yf[e];
           float c = g[e], dc = 1.0f;
           if (a.sigmoid) sigmoid_grad(g[e], c, dc);
-          dg[e] = a.alpha * dc * d[i][e] * n;
+          dg[e] = a.alpha * dc * d[i][e] * (yf[e] * q * w[e]);
           d[i][e] *= c;
         }
         if (a.dgate_full) store_vec(static_cast<T*>(a.dgate_full) + off, v, Pack<T, V>::of(dg));
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) s2[0] = fmaf(yf[e], (a.w_post ? w[e] : 1.0f) * d[i][e], s2[0]);
+      for (int e = 0; e < V; ++e) s[3] = fmaf(yf[e], w[e] * d[i][e], s[3]);
     }
+    if (depth == 3)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (t + gridDim.x < a.T) first_sums(s, after, off + size_t(gridDim.x) * a.H);
+    block_sum<4>(s, ahead ? red2 : red1);
+    if (a.dgate_tok && threadIdx.x == 0) a.dgate_tok[t] = a.alpha * dat * q * s[3];
     if (a.y) {
-      if (a.w_post || a.gate_tok) block_sum<1>(s2, red2);
-      if (a.dgate_tok && threadIdx.x == 0) a.dgate_tok[t] = a.alpha * dat * q * s2[0];
       const float c = a.alpha * at;
-      const float yc = q * q * (s2[0] * inv_h);  // dy = c q (w_post d - y yc)
+      const float yc = q * q * (s[3] * inv_h);  // dy = c q (w_post d - y yc)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const int v = threadIdx.x + i * nth;
@@ -332,10 +361,11 @@ __global__ void __launch_bounds__(THREADS) k_block_norm_bwd(NormArgs a, int dept
           float yf[V], w[V];
           get(stage, kY, i, off).unpack(yf);
           wp[i].unpack(w);
+          const float cq = c * q;
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            gp[i][e] = fmaf(c * d[i][e], yf[e] * q, gp[i][e]);
-            o[e] = c * q * (w[e] * d[i][e] - yf[e] * yc);
+            gp[i][e] = fmaf(cq * d[i][e], yf[e], gp[i][e]);
+            o[e] = cq * (w[e] * d[i][e] - yf[e] * yc);
           }
         } else {
 #pragma unroll
@@ -344,8 +374,9 @@ __global__ void __launch_bounds__(THREADS) k_block_norm_bwd(NormArgs a, int dept
         if (a.dy) store_vec(static_cast<T*>(a.dy) + off, v, Pack<T, V>::of(o));
       }
     }
-    stage = stage + 1 == depth ? 0 : stage + 1;
-    if (!a.y || !(a.w_post || a.gate_tok)) __syncthreads();  // the next row's first sum reuses red1: the second sum's barrier, or this one, lies between
+    statistics(s);
+    if (depth == 2) fetch(t + 2 * gridDim.x, stage);
+    stage = after;
   }
   // partial rows: [gridDim.x][2][H]
   float* part = a.part + size_t(blockIdx.x) * 2 * a.H;
@@ -380,12 +411,7 @@ __global__ void __launch_bounds__(1024) k_norm_weight_sum(const float* __restric
 // ---------------------------------------------------------------- launchers
 int round32(int n) { return (n + 31) / 32 * 32; }
 
-// Persistent CTAs per SM of the backward pass: 768 threads (80 registers each), at most 8 CTAs.
 constexpr int kSms = 148;
-int bwd_per_sm(int threads) {
-  const int n = 768 / threads;
-  return n < 1 ? 1 : n > 8 ? 8 : n;
-}
 
 NormArgs args_of(const moe_block_norm_t& b, int T, int H) {
   NormArgs a = {};
@@ -424,28 +450,17 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Threads and vectors per thread of a backward row, and with them the grid.
-template <typename T, int V>
-int bwd_width(int H) {
-  const int nv = H / V;
-  return nv <= 1024 ? 1 : nv <= 4096 ? 4 : 16;
-}
-template <typename T, int V>
-int bwd_grid(int T_, int H) {
-  const int nv = (H + V - 1) / V, w = bwd_width<T, V>(H), grid = kSms * bwd_per_sm(round32((nv + w - 1) / w));
-  return T_ < grid ? T_ : grid;
-}
-
-// bytes of a stage: a row of every array
-template <typename T, int V>
-int bwd_stage(const NormArgs& a) {
-  const int w = bwd_width<T, V>(a.H);
-  return (a.gate_full ? kArrays : kArrays - 1) * w * round32((a.H / V + w - 1) / w) * int(sizeof(Pack<T, V>));
+// Vectors per thread of a backward row, the thread count its kernel is built for, and the grid.
+int bwd_width(int nv) { return nv <= 512 ? 1 : nv <= 1024 ? 2 : nv <= 4096 ? 4 : 16; }
+int bwd_threads(int nv) { return nv <= 128 ? 128 : nv <= 256 ? 256 : nv <= 1024 ? 512 : 1024; }
+int bwd_grid(int T, int nv) {
+  const int grid = kSms * bwd_ctas(bwd_threads(nv));
+  return T < grid ? T : grid;
 }
 constexpr int kSmemMax = 224 * 1024;
 
 template <typename T, int V, int W, int THREADS, bool DIRECT>
-cudaError_t run_bwd(const NormArgs& a, cudaStream_t st) {
+cudaError_t run_bwd(const NormArgs& a, int grid, cudaStream_t st) {
   // raised once per device, so no later call (e.g. one inside a stream capture) sets attributes
   static std::atomic<bool> done[128] = {};
   int dev = 0;
@@ -457,27 +472,30 @@ cudaError_t run_bwd(const NormArgs& a, cudaStream_t st) {
     if (err != cudaSuccess) return err;
     done[dev].store(true, std::memory_order_release);
   }
-  const int threads = round32((a.H / V + W - 1) / W), stage = bwd_stage<T, V>(a);
-  const int room = kSmemMax / bwd_per_sm(threads);
-  const int depth = DIRECT ? 0 : 3 * stage <= room ? 3 : 2 * stage <= room ? 2 : 1;
-  k_block_norm_bwd<T, V, W, THREADS, DIRECT><<<unsigned(bwd_grid<T, V>(a.T, a.H)), threads, size_t(depth) * stage, st>>>(a, depth);
+  const int threads = round32((a.H / V + W - 1) / W), stage = bwd_stage_bytes<T, V, W, THREADS>(a.gate_full != nullptr);
+  const int depth = DIRECT || 3 * stage > kSmemMax / bwd_ctas(THREADS) ? 2 : 3;
+  k_block_norm_bwd<T, V, W, THREADS, DIRECT><<<unsigned(grid), threads, DIRECT ? 0 : size_t(depth) * stage, st>>>(a, depth);
   return cudaGetLastError();
 }
 
 template <typename T, int V>
 cudaError_t norm_bwd(const NormArgs& a, int* grid, cudaStream_t st) {
-  *grid = bwd_grid<T, V>(a.T, a.H);
-  const int w = bwd_width<T, V>(a.H);
-  const int nv = a.H / V;
-  if (w == 1) {
-    if (nv <= 768) return run_bwd<T, V, 1, 768, false>(a, st);
-    return nv <= 896 ? run_bwd<T, V, 1, 896, false>(a, st) : run_bwd<T, V, 1, 1024, false>(a, st);
-  }
+  const int nv = a.H / V, g = bwd_grid(a.T, nv);
+  *grid = g;
+  if (nv <= 128) return run_bwd<T, V, 1, 128, false>(a, g, st);
+  if (nv <= 256) return run_bwd<T, V, 1, 256, false>(a, g, st);
+  if (nv <= 512) return run_bwd<T, V, 1, 512, false>(a, g, st);
+  if (nv <= 1024) return run_bwd<T, V, 2, 512, false>(a, g, st);
   // H <= 16384: at most 512 threads of four 8-element vectors, 1024 of narrower ones
-  const bool direct = bwd_stage<T, V>(a) > kSmemMax;
   constexpr int most = V == 8 ? 512 : 1024;
-  if (w == 4) return direct ? run_bwd<T, V, 4, most, true>(a, st) : run_bwd<T, V, 4, most, false>(a, st);
-  if constexpr (V == 1) return direct ? run_bwd<T, V, 16, 1024, true>(a, st) : run_bwd<T, V, 16, 1024, false>(a, st);
+  if (nv <= 4096) {
+    if (2 * bwd_stage_bytes<T, V, 4, most>(a.gate_full != nullptr) > kSmemMax) return run_bwd<T, V, 4, most, true>(a, g, st);
+    return run_bwd<T, V, 4, most, false>(a, g, st);
+  }
+  if constexpr (V == 1) {
+    if (2 * bwd_stage_bytes<T, V, 16, 1024>(a.gate_full != nullptr) > kSmemMax) return run_bwd<T, V, 16, 1024, true>(a, g, st);
+    return run_bwd<T, V, 16, 1024, false>(a, g, st);
+  }
   return cudaErrorInvalidValue;
 }
 
@@ -510,12 +528,10 @@ cudaError_t launch_block_norm(const moe_block_norm_t& b, const void* x, int T, i
   return norm_any(a, dt, nullptr, st);
 }
 
-// the largest grid over the element types and alignments
+// the largest grid over the element types and alignments: the fewer vectors a row has, the more CTAs
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H) {
   const int t = T < INT_MAX ? int(T) : INT_MAX, h = H < 16384 ? int(H) : 16384;
-  int g = 0;
-  for (int n : {bwd_grid<__nv_bfloat16, 8>(t, h), bwd_grid<float, 4>(t, h), bwd_grid<float, 1>(t, h)}) g = n > g ? n : g;
-  return size_t(g) * 2 * size_t(H) * sizeof(float);
+  return size_t(bwd_grid(t, (h + 7) / 8)) * 2 * size_t(H) * sizeof(float);
 }
 
 cudaError_t launch_block_norm_bwd(const moe_block_norm_t& b, const void* z, const void* dz, const void* dh, int T, int H,

@@ -24,6 +24,7 @@ MOE_DEVICE float from_float<float>(float f) {
   return f;
 }
 
+// Two 16-bit elements of a register, and back (rounded to nearest even).
 MOE_DEVICE void unpack2(uint32_t w, float& lo, float& hi, __nv_bfloat16) {
   lo = bf16_lo(w);
   hi = bf16_hi(w);
@@ -33,32 +34,67 @@ MOE_DEVICE void unpack2(uint32_t w, float& lo, float& hi, __half) {
   lo = v.x;
   hi = v.y;
 }
+MOE_DEVICE uint32_t pack2(float lo, float hi, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+MOE_DEVICE uint32_t pack2(float lo, float hi, __half) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
-// V elements as they lie in memory (kept packed while a load is in flight).
+// V elements as they lie in memory (kept packed while a load is in flight): V * sizeof(T) is 16, or V = 1.
+template <int BYTES>
+struct RawOf;
+template <>
+struct RawOf<16> {
+  using type = uint4;
+};
+template <>
+struct RawOf<4> {
+  using type = uint32_t;
+};
+template <>
+struct RawOf<2> {
+  using type = uint16_t;
+};
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-  T e[V];
+struct Pack {
+  using Raw = typename RawOf<V * int(sizeof(T))>::type;
+  Raw raw;
   MOE_DEVICE void unpack(float (&f)[V]) const {
-    if constexpr (V == 8) {  // two 16-bit elements per register
-      const uint4 u = *reinterpret_cast<const uint4*>(e);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) unpack2(w[i], f[2 * i], f[2 * i + 1], T());
+    if constexpr (V == 8) {
+      unpack2(raw.x, f[0], f[1], T());
+      unpack2(raw.y, f[2], f[3], T());
+      unpack2(raw.z, f[4], f[5], T());
+      unpack2(raw.w, f[6], f[7], T());
+    } else if constexpr (V == 4) {
+      f[0] = __uint_as_float(raw.x);
+      f[1] = __uint_as_float(raw.y);
+      f[2] = __uint_as_float(raw.z);
+      f[3] = __uint_as_float(raw.w);
     } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = to_float(e[i]);
+      f[0] = to_float(*reinterpret_cast<const T*>(&raw));
     }
   }
   MOE_DEVICE static Pack of(const float (&f)[V]) {
     Pack p;
-#pragma unroll
-    for (int i = 0; i < V; ++i) p.e[i] = from_float<T>(f[i]);
+    if constexpr (V == 8) {
+      p.raw = make_uint4(pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()), pack2(f[6], f[7], T()));
+    } else if constexpr (V == 4) {
+      p.raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {
+      const T v = from_float<T>(f[0]);
+      p.raw = *reinterpret_cast<const Raw*>(&v);
+    }
     return p;
   }
   MOE_DEVICE static Pack zero() {
     Pack p;
-#pragma unroll
-    for (int i = 0; i < V; ++i) p.e[i] = from_float<T>(0.0f);
+    if constexpr (V > 1)
+      p.raw = make_uint4(0, 0, 0, 0);
+    else
+      p.raw = 0;
     return p;
   }
 };
@@ -67,27 +103,26 @@ struct alignas(sizeof(T) * V) Pack {
 // that aliases its input).
 template <typename T, int V>
 MOE_DEVICE Pack<T, V> load_vec(const T* row, int v) {
-  return *reinterpret_cast<const Pack<T, V>*>(row + size_t(v) * V);
+  Pack<T, V> p;
+  p.raw = *reinterpret_cast<const typename Pack<T, V>::Raw*>(row + size_t(v) * V);
+  return p;
 }
 // The same through the read-only path, for data that no one writes during the call; the line
 // is not kept in L1 (each row is read once).
 template <typename T, int V>
 MOE_DEVICE Pack<T, V> load_vec_once(const T* row, int v) {
   Pack<T, V> p;
-  if constexpr (sizeof(p) == 16) {
-    uint4 u;
+  if constexpr (V > 1)
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "=r"(p.raw.x), "=r"(p.raw.y), "=r"(p.raw.z), "=r"(p.raw.w)
                  : "l"(row + size_t(v) * V));
-    p = *reinterpret_cast<const Pack<T, V>*>(&u);
-  } else {
-    p = *reinterpret_cast<const Pack<T, V>*>(row + size_t(v) * V);
-  }
+  else
+    p.raw = __ldg(reinterpret_cast<const typename Pack<T, V>::Raw*>(row + v));
   return p;
 }
 template <typename T, int V>
 MOE_DEVICE void store_vec(T* row, int v, const Pack<T, V>& p) {
-  *reinterpret_cast<Pack<T, V>*>(row + size_t(v) * V) = p;
+  *reinterpret_cast<typename Pack<T, V>::Raw*>(row + size_t(v) * V) = p.raw;
 }
 
 MOE_DEVICE float warp_sum(float v) {
