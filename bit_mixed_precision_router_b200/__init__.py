@@ -670,12 +670,14 @@ def _device_of(*tensors) -> int:
     return dev
 
 
-def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+def _new(like: torch.Tensor, dtype, stream, *size) -> torch.Tensor:
     """An output on the device of `like` that belongs to the stream the call runs on."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return like.new_empty(*size, dtype=dtype)
+    if dtype is like.dtype:
+        return like.new_empty(*size)
+    return like.new_empty(*size, dtype=dtype)
 
 
 def _call_on(device: int, stream, name: str, *args) -> None:
@@ -800,7 +802,7 @@ def moe_linear_w4(x: torch.Tensor, w: Linear, act: int = ACT_NONE, residual: tor
     if T > 1 and ldy < M:
         raise ValueError("out: its rows overlap")
     dev = _device_of(x, w.w, w.scale, w.gscale, residual, out)
-    y = _new(x, (T, M), dt, stream) if out is None else out
+    y = _new(x, dt, stream, T, M) if out is None else out
     wc = LinearT(w.fmt, _p(w.w), _p(w.scale), _p(w.gscale))
     _call_on(dev, stream, "moe_linear_w4", x.data_ptr(), ldx, DTYPES[x.dtype], ctypes.byref(wc), T, N, K, act,
              None if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, DTYPES[dt])
@@ -826,7 +828,7 @@ def moe_permute_capacity(ids: torch.Tensor, T: int, k: int, E: int, capacity: in
     dev = _device_of(ids)
     if out is None:
         P = max(T * k, 1)
-        i32 = [_new(ids, n, torch.int32, stream) for n in (E + 1, P, P, E + 1)]
+        i32 = [_new(ids, torch.int32, stream, n) for n in (E + 1, P, P, E + 1)]
         out = Routing(ids, None, *i32)
     else:
         _check(out.sorted_pair, "sorted_pair", torch.int32, T * k)
@@ -849,7 +851,7 @@ def moe_sort_rows(x: torch.Tensor, routing: Routing, k: int, weighted: bool = Fa
     _matrix(rows, "rows", x.dtype, T * k, H)
     rc = _pairs(routing, T, k, weighted)
     dev = _device_of(x, rows, routing.pair_to_row, routing.topk_w if weighted else None)
-    rows = _new(x, (max(T * k, 1), H), x.dtype, stream) if rows is None else rows
+    rows = _new(x, x.dtype, stream, max(T * k, 1), H) if rows is None else rows
     _call_on(dev, stream, "moe_sort_rows", _p(x), code, ctypes.byref(rc), int(weighted), T, H, k, _p(rows))
     return rows
 
@@ -873,7 +875,7 @@ def moe_unsort_rows(rows: torch.Tensor, routing: Routing, T: int, k: int, weight
     _matrix(out, "out", rows.dtype, T, H)
     rc = _pairs(routing, T, k, weighted)
     dev = _device_of(rows, residual, out, routing.pair_to_row, routing.topk_w if weighted else None)
-    out = _new(rows, (T, H), rows.dtype, stream) if out is None else out
+    out = _new(rows, rows.dtype, stream, T, H) if out is None else out
     _call_on(dev, stream, "moe_unsort_rows", _p(rows), code, ctypes.byref(rc), int(weighted), _p(residual), T, H, k,
              _p(out))
     return out
@@ -902,9 +904,9 @@ def _rows_bwd(name, a, routing, T, H, k, other, other_name, other_rows, weighted
     rc = _pairs(routing, T, k, weighted)
     dev = _device_of(a, other, out, dw, routing.pair_to_row, routing.topk_w if weighted else None)
     if out is None:
-        out = _new(a, (max(out_rows, 1) if out_name == "d_rows" else T, H), a.dtype, stream)
+        out = _new(a, a.dtype, stream, max(out_rows, 1) if out_name == "d_rows" else T, H)
     if dw is None and other is not None:
-        dw = _new(a, T * k, torch.float32, stream)
+        dw = _new(a, torch.float32, stream, T * k)
     _call_on(dev, stream, name, _p(a), code, ctypes.byref(rc), int(weighted), _p(other), T, H, k, _p(out), _p(dw))
     return out, dw
 
@@ -917,7 +919,7 @@ def moe_route_topk_bwd(dw: torch.Tensor, routing: Routing, T: int, E: int, k: in
     _check(routing.topk_w, "topk_w", torch.float32, T * k)
     _matrix(d_logits, "d_logits", torch.float32, T, E)
     dev = _device_of(dw, routing.topk_ids, routing.topk_w, d_logits)
-    d_logits = _new(dw, (T, E), torch.float32, stream) if d_logits is None else d_logits
+    d_logits = _new(dw, torch.float32, stream, T, E) if d_logits is None else d_logits
     rc = RoutingT(_p(routing.topk_ids), _p(routing.topk_w), None, None, None, None)
     _call_on(dev, stream, "moe_route_topk_bwd", _p(dw), ctypes.byref(rc), T, E, k, _p(d_logits))
     return d_logits
@@ -939,10 +941,10 @@ def _norm_step(x, y, routing, k, w_post, gate, gate_sigmoid, alpha, w_next, eps)
     mode = GATE_NONE
     if gate is not None:
         mode = GATE_TOKEN if gate.dim() == 1 else GATE_FULL
-        if mode == GATE_TOKEN:
-            _check(gate, "gate", torch.float32, T)
-        else:
-            _matrix(gate, "gate", x.dtype, T, H)
+        if gate.dtype != (torch.float32 if mode == GATE_TOKEN else x.dtype):
+            raise TypeError(f"gate: got {gate.dtype}")
+        if gate.shape != ((T,) if mode == GATE_TOKEN else (T, H)):
+            raise ValueError(f"gate: expected {(T,)} or {(T, H)}, has {tuple(gate.shape)}")
     row = w = None
     if routing is not None:
         _check(routing.pair_to_row, "pair_to_row", torch.int32, T * k)
@@ -969,9 +971,9 @@ def moe_block_norm(x: torch.Tensor, y: torch.Tensor | None = None, routing: Rout
     _matrix(h, "h", x.dtype, T, H)
     _device_of(x, z, h)
     if z is None and y is not None:
-        z = _new(x, (T, H), x.dtype, stream)
+        z = _new(x, x.dtype, stream, T, H)
     if h is None and w_next is not None:
-        h = _new(x, (T, H), x.dtype, stream)
+        h = _new(x, x.dtype, stream, T, H)
     _call_on(dev, stream, "moe_block_norm", ctypes.byref(step), _p(x), code, T, H, _p(z), _p(h))
     return z, h
 
@@ -1006,17 +1008,19 @@ def moe_block_norm_bwd(z: torch.Tensor, dz: torch.Tensor | None = None, dh: torc
     _matrix(dh, "dh", z.dtype, T, H)
     _device_of(z, dz, dh, workspace)
     f32 = torch.float32
-    g = BlockNormGrads(_new(z, (T, H), z.dtype, stream))
+    g = BlockNormGrads(_new(z, z.dtype, stream, T, H))
     if y is not None:
-        g.dy = _new(z, (T, H), z.dtype, stream)
+        g.dy = _new(z, z.dtype, stream, T, H)
     if gate is not None:
-        g.dgate = _new(z, T if gate.dim() == 1 else (T, H), gate.dtype, stream)
-    if w_post is not None:
-        g.dw_post = _new(z, H, f32, stream)
-    if dh is not None:
-        g.dw_next = _new(z, H, f32, stream)
+        g.dgate = _new(gate, gate.dtype, stream, *gate.shape)
+    if w_post is not None and dh is not None:
+        g.dw_post, g.dw_next = _new(z, f32, stream, 2, H).unbind()
+    elif w_post is not None:
+        g.dw_post = _new(z, f32, stream, H)
+    elif dh is not None:
+        g.dw_next = _new(z, f32, stream, H)
     if workspace is None:
-        workspace = _new(z, max(moe_block_norm_bwd_workspace_bytes(T, H), 16), torch.uint8, stream)
+        workspace = _new(z, torch.uint8, stream, max(moe_block_norm_bwd_workspace_bytes(T, H), 16))
     gc = BlockNormGradsT(_p(g.dx), _p(g.dy), _p(g.dgate), _p(g.dw_post), _p(g.dw_next))
     _call_on(dev, stream, "moe_block_norm_bwd", ctypes.byref(step), _p(z), _p(dz), _p(dh), code, T, H, ctypes.byref(gc),
              _p(workspace), workspace.numel() * workspace.element_size())

@@ -3,7 +3,8 @@
 
 namespace moe {
 
-cudaError_t linear_nvfp4(const LinearArgs& a, bool bf16, cudaStream_t st);  // moe_linear_nvfp4.cu
+cudaError_t linear_nvfp4(const LinearArgs& a, bool bf16, cudaStream_t st);                    // moe_linear_nvfp4.cu
+cudaError_t linear_umma(const LinearArgs& a, moe_format_t fmt, bool bf16, cudaStream_t st);  // moe_linear_umma.cu
 
 cudaError_t launch_linear_w4(const moe_linear_t& w, const void* x, int64_t ldx, moe_dtype_t x_dtype, int T, int N, int K,
                              moe_act_t act, const void* residual, int64_t ldr, void* y, int64_t ldy, moe_dtype_t y_dtype,
@@ -24,6 +25,8 @@ cudaError_t launch_linear_w4(const moe_linear_t& w, const void* x, int64_t ldx, 
   a.K = K;
   a.swiglu = act == MOE_ACT_SWIGLU;
   const bool bf16 = x_dtype == MOE_BF16;
+  // UMMA_OVERRIDE
+  if (T > 16) return linear_umma(a, w.fmt, bf16, st);
   if (w.fmt == MOE_FMT_W4G128)
     return bf16 ? pick_linear<true, MOE_FMT_W4G128>(a, st) : pick_linear<false, MOE_FMT_W4G128>(a, st);
   return linear_nvfp4(a, bf16, st);

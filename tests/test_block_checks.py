@@ -195,6 +195,12 @@ def test_binding_norms():
         moe.moe_block_norm(x, w_post=w)
     with pytest.raises(ValueError, match="gate"):
         moe.moe_block_norm(x, x, gate=torch.zeros(3))
+    with pytest.raises(ValueError, match="gate"):
+        moe.moe_block_norm(x, x, gate=torch.zeros(5))
+    with pytest.raises(ValueError, match="gate"):
+        moe.moe_block_norm(x, x, gate=torch.zeros((4, 1)))
+    with pytest.raises(TypeError, match="gate"):
+        moe.moe_block_norm(x.half(), x.half(), gate=torch.zeros(4).half())
     with pytest.raises(TypeError, match="gate"):
         moe.moe_block_norm(x.half(), x.half(), gate=torch.zeros((4, 64)))
     with pytest.raises(ValueError, match="y"):
