@@ -25,11 +25,39 @@ namespace cg = cooperative_groups;
 constexpr int kRowThreads = 256;
 constexpr int kSlots = 8;  // rows of a token in flight per thread
 
+// Sums of N values over the CTA (N a power of two up to 32), in one fixed order; value j is returned to thread j < N.  Each
+// step of the warp's butterfly halves the values a lane carries (N - 1 + log2(32 / N) exchanges instead of 5 N), the warps'
+// sums meet in shared memory (`red`: N * 8 floats; at most 8 warps).
+template <int N>
+MOE_DEVICE float block_sums(float (&v)[N], float* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int w = 16;
+#pragma unroll
+  for (int n = N; n > 1; n /= 2, w /= 2) {
+    const bool upper = lane & w;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float give = upper ? v[i] : v[n / 2 + i], keep = upper ? v[n / 2 + i] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+    }
+  }
+#pragma unroll
+  for (; w >= 1; w /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+  if (lane % (32 / N) == 0) red[(lane / (32 / N)) * 8 + warp] = v[0];
+  __syncthreads();
+  float s = 0.0f;
+  if (threadIdx.x < N) {
+#pragma unroll
+    for (int i = 0; i < kRowThreads / 32; ++i) s += i < nw ? red[threadIdx.x * 8 + i] : 0.0f;
+  }
+  return s;
+}
+
 template <typename T, int V, bool DOT>
-__global__ void __launch_bounds__(kRowThreads) k_spread(const T* a, const T* __restrict__ b, const float* __restrict__ w,
+__global__ void __launch_bounds__(kRowThreads, DOT ? 3 : 0) k_spread(const T* a, const T* __restrict__ b, const float* __restrict__ w,
                                                         const int32_t* __restrict__ p2r, int H, int k,
                                                         T* __restrict__ rows, float* __restrict__ dw) {
-  __shared__ float red[kSlots * 32];
+  __shared__ float red[kSlots * 8];
   const int t = blockIdx.x, nv = H / V;
   const T* arow = a + size_t(t) * H;
   const int step = DOT ? int(blockDim.x) : int(blockDim.x * gridDim.y);
@@ -74,10 +102,9 @@ __global__ void __launch_bounds__(kRowThreads) k_spread(const T* a, const T* __r
       }
     }
     if (DOT) {
-      block_sum<kSlots>(dot, red);
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j)
-        if (threadIdx.x == j && j0 + j < k) dw[size_t(t) * k + j0 + j] = dot[j];
+      const float s = block_sums<kSlots>(dot, red);
+      const int j = j0 + int(threadIdx.x);
+      if (threadIdx.x < kSlots && j < k) dw[size_t(t) * k + j] = s;
       __syncthreads();
     }
   }
@@ -85,10 +112,10 @@ __global__ void __launch_bounds__(kRowThreads) k_spread(const T* a, const T* __r
 
 // KB: slots unrolled (k <= KB).
 template <typename T, int V, bool DOT, int KB>
-__global__ void __launch_bounds__(kRowThreads) k_gather(const T* __restrict__ rows, const T* x, const float* __restrict__ w,
+__global__ void __launch_bounds__(kRowThreads, DOT && KB == kSlots ? 3 : 0) k_gather(const T* __restrict__ rows, const T* x, const float* __restrict__ w,
                                                         const int32_t* __restrict__ p2r, int H, int k, T* out,
                                                         float* __restrict__ dw) {
-  __shared__ float red[KB * 32];
+  __shared__ float red[KB * 8];
   __shared__ int srow[KB];
   __shared__ float sw[KB];
   const int t = blockIdx.x, nv = H / V;
@@ -139,10 +166,8 @@ __global__ void __launch_bounds__(kRowThreads) k_gather(const T* __restrict__ ro
     store_vec(out + size_t(t) * H, v, Pack<T, V>::of(acc));
   }
   if (DOT) {
-    block_sum<KB>(dot, red);
-#pragma unroll
-    for (int j = 0; j < KB; ++j)
-      if (threadIdx.x == j && j < k) dw[size_t(t) * k + j] = dot[j];
+    const float s = block_sums<KB>(dot, red);
+    if (threadIdx.x < KB && int(threadIdx.x) < k) dw[size_t(t) * k + threadIdx.x] = s;
   }
 }
 
