@@ -440,7 +440,7 @@ moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, cons
 // check_route_shape without k <= E: with dropped pairs a token may choose experts of other ranks
 static moe_status_t check_pairs_shape(int64_t T, int64_t E, int64_t k) {
   if (T < 0) return MOE_ERR_INVALID_ARG;
-  if (E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || T > INT_MAX / k) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || T > (1 << 30) / k) return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
 
@@ -464,7 +464,7 @@ moe_status_t moe_permute_capacity(const int32_t* ids, int64_t T, int64_t k, int6
 static moe_status_t check_rows(moe::RowArgs* g, moe_dtype_t dt, const moe_routing_t* routing, int weighted, int64_t T,
                                int64_t H, int64_t k) {
   if (!dtype_ok(dt) || T < 0 || k < 1 || H < 1) return MOE_ERR_INVALID_ARG;
-  if (k > MOE_MAX_TOPK || H > (1 << 20) || T > INT_MAX / k) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (k > MOE_MAX_TOPK || H > (1 << 20) || T > (1 << 30) / k) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
   if (!routing || !routing->pair_to_row || (weighted && !routing->topk_w) || !g->a || !g->out) return MOE_ERR_INVALID_ARG;
   const size_t es = dtype_size(dt);
@@ -552,7 +552,7 @@ static moe_status_t check_norm(const moe_block_norm_t* b, moe_dtype_t dt, int64_
   if (!b->y && (b->w_post || b->gate || b->pair_to_row)) return MOE_ERR_INVALID_ARG;
   if (b->pair_to_row) {
     if (b->k < 1) return MOE_ERR_INVALID_ARG;
-    if (b->k > MOE_MAX_TOPK || T > INT_MAX / b->k) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (b->k > MOE_MAX_TOPK || T > (1 << 30) / b->k) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (!aligned_to(b->pair_to_row, 4) || !aligned_to(b->topk_w, 4)) return MOE_ERR_MISALIGNED;
   }
   const size_t es = dtype_size(dt);

@@ -450,8 +450,8 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Vectors per thread of a backward row, the thread count its kernel is built for, and the grid.
-int bwd_width(int nv) { return nv <= 512 ? 1 : nv <= 1024 ? 2 : nv <= 4096 ? 4 : 16; }
+// The thread count a backward row's kernel is built for (one vector per thread up to 512 vectors, two up to 1024, four or
+// sixteen beyond), and the grid.
 int bwd_threads(int nv) { return nv <= 128 ? 128 : nv <= 256 ? 256 : nv <= 1024 ? 512 : 1024; }
 int bwd_grid(int T, int nv) {
   const int grid = kSms * bwd_ctas(bwd_threads(nv));

@@ -461,8 +461,10 @@ typedef enum {
  *   elements apart; ldr = 0: one row for all tokens (a bias).  y may be residual (with ldy = ldr).
  * Requires K % 128 == 0, 1 <= N <= 2^30, K <= 2^20, N even with SwiGLU, ldx >= K and
  * ldx % 8 == 0, ldy >= M, ldr = 0 or >= M; x, w, scale 16-byte aligned, y and residual aligned to their
- * element.  Any T >= 0; the weights are read once per 64 tokens: made for decode batches (larger
- * batches of whole experts are moe_grouped_ffn's, which takes E = 1). */
+ * element; y overlaps no other input.  Any T from 0 to 2^22 - 64; the weights are read once per 64
+ * tokens: made for decode batches (larger batches of whole experts are moe_grouped_ffn's, which takes
+ * E = 1).  The first call on a device sets kernel attributes: make one call per shape to be
+ * captured before a stream capture. */
 moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, const moe_linear_t* w, int64_t T, int64_t N,
                            int64_t K, moe_act_t act, const void* residual, int64_t ldr, void* y, int64_t ldy,
                            moe_dtype_t y_dtype, moe_stream_t stream);
@@ -476,7 +478,7 @@ moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, cons
  * Of the routing only pair_to_row is read (and topk_w where weighted), 4-byte aligned.
  * Row buffers need only their element's alignment: 128-bit accesses are used when they start on
  * 16 bytes and H is a multiple of 16 bytes, else single elements.  Rows that no pair refers to are
- * left as they are.  1 <= H <= 2^20, 1 <= k <= MOE_MAX_TOPK.  Outputs must not overlap inputs,
+ * left as they are.  1 <= H <= 2^20, 1 <= k <= MOE_MAX_TOPK, T * k <= 2^30.  Outputs must not overlap inputs,
  * except that out may be residual.  Deterministic.
  * ------------------------------------------------------------------------ */
 
@@ -489,7 +491,7 @@ moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, cons
  * computed), the calls below and moe_combine (a dropped pair adds nothing); not
  * moe_grouped_ffn_w4a4, whose activation scale spans all T*k rows.
  *   ids int32 [T*k], 4-byte aligned; capacity >= 0 (0: no limit); 1 <= E <= MOE_MAX_EXPERTS,
- *   1 <= k <= MOE_MAX_TOPK (k may exceed E).  T = 0: nothing is written. */
+ *   1 <= k <= MOE_MAX_TOPK (k may exceed E), T * k <= 2^30.  T = 0: nothing is written. */
 moe_status_t moe_permute_capacity(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t capacity,
                                   const moe_routing_t* out, moe_stream_t stream);
 
@@ -586,7 +588,7 @@ size_t moe_block_norm_bwd_workspace_bytes(int64_t T, int64_t H);
  * the step does not have (dy without y, dgate without gate, dw_post without w_post, dw_next without dh)
  * must be NULL.  Workspace: at least moe_block_norm_bwd_workspace_bytes(T, H), 16-byte aligned, contents
  * need not be initialised; calls that overlap on one workspace race.  T = 0 writes zeros to dw_post
- * and dw_next. */
+ * and dw_next.  The first call on a device sets kernel attributes: make one before a stream capture. */
 moe_status_t moe_block_norm_bwd(const moe_block_norm_t* step, const void* z, const void* dz, const void* dh,
                                 moe_dtype_t dtype, int64_t T, int64_t H, const moe_block_norm_grads_t* grads,
                                 void* workspace, size_t workspace_bytes, moe_stream_t stream);
