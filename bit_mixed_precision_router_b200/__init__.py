@@ -689,11 +689,14 @@ def _call_on(device: int, stream, name: str, *args) -> None:
         if stream.device.index != device:
             raise ValueError(f"stream of {stream.device} with tensors on device {device}")
         raw = stream.cuda_stream
+    fn = getattr(_lib or load(), name)
     if torch._C._cuda_getDevice() == device:
-        _call(name, *args, raw)
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            _call(name, *args, raw)
+            st = fn(*args, raw)
+    if st != 0:
+        raise MoeError(name, st)
 
 
 def _dtype_code(t: torch.Tensor, what: str) -> int:

@@ -280,9 +280,9 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
   fetch(blockIdx.x + gridDim.x, 1);
   asm volatile("cp.async.wait_group 1;" ::: "memory");
   {
-    float s[3] = {0.0f, 0.0f, 0.0f};
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     first_sums(s, 0, size_t(blockIdx.x) * a.H);
-    block_sum<3>(s, red1);
+    block_sum<4>(s, red1);
     statistics(s);
   }
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, ahead ^= 1) {

@@ -25,25 +25,13 @@ namespace cg = cooperative_groups;
 constexpr int kRowThreads = 256;
 constexpr int kSlots = 8;  // rows of a token in flight per thread
 
-// Sums of N values over the CTA (N a power of two up to 32), in one fixed order; value j is returned to thread j < N.  Each
-// step of the warp's butterfly halves the values a lane carries (N - 1 + log2(32 / N) exchanges instead of 5 N), the warps'
-// sums meet in shared memory (`red`: N * 8 floats; at most 8 warps).
+// Sums of N values over the CTA (at most kRowThreads threads), in one fixed order; value j is returned to thread j < N.
+// `red`: 8 N floats of shared memory.
 template <int N>
 MOE_DEVICE float block_sums(float (&v)[N], float* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int w = 16;
-#pragma unroll
-  for (int n = N; n > 1; n /= 2, w /= 2) {
-    const bool upper = lane & w;
-#pragma unroll
-    for (int i = 0; i < n / 2; ++i) {
-      const float give = upper ? v[i] : v[n / 2 + i], keep = upper ? v[n / 2 + i] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
-    }
-  }
-#pragma unroll
-  for (; w >= 1; w /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
-  if (lane % (32 / N) == 0) red[(lane / (32 / N)) * 8 + warp] = v[0];
+  const float w = warp_sums<N>(v);
+  if (lane % (32 / N) == 0) red[(lane / (32 / N)) * 8 + warp] = w;
   __syncthreads();
   float s = 0.0f;
   if (threadIdx.x < N) {

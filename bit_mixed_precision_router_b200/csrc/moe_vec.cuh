@@ -51,6 +51,10 @@ struct RawOf<16> {
   using type = uint4;
 };
 template <>
+struct RawOf<8> {
+  using type = uint2;
+};
+template <>
 struct RawOf<4> {
   using type = uint32_t;
 };
@@ -131,21 +135,45 @@ MOE_DEVICE float warp_sum(float v) {
   return v;
 }
 
-// Sums of N values over the CTA (blockDim.x a multiple of 32), in one fixed order.  `red`:
-// 32 * N floats of shared memory that no earlier sum of the same iteration used.
+// The warp's sums of N values (N a power of two up to 32): lane l returns the sum of value l / (32 / N).  Each step of the
+// butterfly halves the values a lane carries: N - 1 + log2(32 / N) exchanges instead of 5 N.
+template <int N>
+MOE_DEVICE float warp_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int w = 16;
+#pragma unroll
+  for (int n = N; n > 1; n /= 2, w /= 2) {
+    const bool upper = lane & w;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float give = upper ? v[i] : v[n / 2 + i], keep = upper ? v[n / 2 + i] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+    }
+  }
+#pragma unroll
+  for (; w >= 1; w /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+  return v[0];
+}
+
+// Sums of N values (1, 2 or 4) over the CTA (blockDim.x a multiple of 32, at most 1024), in one fixed order, to every
+// thread.  `red`: 32 * N floats of shared memory that no sum wrote since the barrier before last.
 template <int N>
 MOE_DEVICE void block_sum(float (&v)[N], float* red) {
+  constexpr int L = 32 / N;  // lanes per value
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  float s = warp_sums<N>(v);
+  if (nw > 1) {
+    if (lane % L == 0) red[(lane / L) * 32 + warp] = s;
+    __syncthreads();
+    s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (nw == 1) return;
-  if (lane == 0) {
+    for (int w = 0; w < N; ++w)
+      if (lane % L + w * L < nw) s += red[(lane / L) * 32 + lane % L + w * L];
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[i * 32 + warp] = v[i];
+    for (int d = L / 2; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   }
-  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < nw ? red[i * 32 + lane] : 0.0f);
+  for (int i = 0; i < N; ++i) v[i] = N > 1 ? __shfl_sync(0xffffffffu, s, i * L) : s;
 }
 
 template <typename T>
