@@ -1016,11 +1016,9 @@ def moe_block_norm_bwd(z: torch.Tensor, dz: torch.Tensor | None = None, dh: torc
         g.dy = _new(z, z.dtype, stream, T, H)
     if gate is not None:
         g.dgate = _new(gate, gate.dtype, stream, *gate.shape)
-    if w_post is not None and dh is not None:
-        g.dw_post, g.dw_next = _new(z, f32, stream, 2, H).unbind()
-    elif w_post is not None:
+    if w_post is not None:
         g.dw_post = _new(z, f32, stream, H)
-    elif dh is not None:
+    if dh is not None:
         g.dw_next = _new(z, f32, stream, H)
     if workspace is None:
         workspace = _new(z, torch.uint8, stream, max(moe_block_norm_bwd_workspace_bytes(T, H), 16))

@@ -192,13 +192,16 @@ __host__ __device__ constexpr int bwd_stage_bytes(bool gate) {
   return (gate ? kArrays : kArrays - 1) * W * THREADS * int(sizeof(Pack<T, V>));
 }
 
-// DIRECT: rows too long for two stages are read from global memory (the second reading from L2).
-template <typename T, int V, int W, int THREADS, bool DIRECT>
+// FULL: a step with dz, dh, y, w_post and the gradients of x and y, and no elementwise gate, known to the compiler.  DIRECT: rows
+// too long for two stages are read from global memory (the second reading from L2).
+template <typename T, int V, int W, int THREADS, bool DIRECT, bool FULL>
 __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(NormArgs a, int depth) {
+  const bool has_dh = FULL || a.dh, has_dz = FULL || a.dz, has_y = FULL || a.y, has_post = FULL || a.w_post;
+  const bool has_dx = FULL || a.dx, has_dy = FULL || a.dy, has_gate = !FULL && a.gate_full;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red1[4 * 32], red2[4 * 32];
   const int nv = a.H / V, nth = blockDim.x;
-  const int stage_bytes = bwd_stage_bytes<T, V, W, THREADS>(a.gate_full != nullptr);
+  const int stage_bytes = bwd_stage_bytes<T, V, W, THREADS>(has_gate);
   const float inv_h = 1.0f / float(a.H);
   uint8_t* const mine = smem + threadIdx.x * sizeof(Pack<T, V>);
   // array and vector at offsets known to the compiler: spaced for THREADS threads, whatever the launch has
@@ -221,13 +224,13 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
       for (int i = 0; i < W; ++i) {
         const int v = threadIdx.x + i * nth;
         if (v >= nv) continue;
-        if (a.dh) {
+        if (has_dh) {
           copy_vec(slot(stage, kZ, i), static_cast<const T*>(a.x) + off, v);
           copy_vec(slot(stage, kDh, i), static_cast<const T*>(a.dh) + off, v);
         }
-        if (a.dz) copy_vec(slot(stage, kDz, i), static_cast<const T*>(a.dz) + off, v);
-        if (a.y) copy_vec(slot(stage, kY, i), static_cast<const T*>(a.y) + off, v);
-        if (a.gate_full) copy_vec(slot(stage, kGate, i), static_cast<const T*>(a.gate_full) + off, v);
+        if (has_dz) copy_vec(slot(stage, kDz, i), static_cast<const T*>(a.dz) + off, v);
+        if (has_y) copy_vec(slot(stage, kY, i), static_cast<const T*>(a.y) + off, v);
+        if (has_gate) copy_vec(slot(stage, kGate, i), static_cast<const T*>(a.gate_full) + off, v);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -237,8 +240,8 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
   for (int i = 0; i < W; ++i) {
     const int v = threadIdx.x + i * nth;
     wn[i] = wp[i] = Pack<T, V>::zero();
-    if (v < nv && a.dh) wn[i] = load_vec<T, V>(static_cast<const T*>(a.w_next), v);
-    if (v < nv && a.w_post) wp[i] = load_vec<T, V>(static_cast<const T*>(a.w_post), v);
+    if (v < nv && has_dh) wn[i] = load_vec<T, V>(static_cast<const T*>(a.w_next), v);
+    if (v < nv && has_post) wp[i] = load_vec<T, V>(static_cast<const T*>(a.w_post), v);
   }
   float gp[W][V], gn[W][V];  // this CTA's sums for dw_post, dw_next
 #pragma unroll
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
     for (int i = 0; i < W; ++i) {
       if (threadIdx.x + i * nth >= nv) continue;
       float zf[V], f[V], w[V];
-      if (a.dh) {
+      if (has_dh) {
         get(stage, kZ, i, off).unpack(zf);
         get(stage, kDh, i, off).unpack(f);
         wn[i].unpack(w);
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
           s[1] = fmaf(zf[e], w[e] * f[e], s[1]);
         }
       }
-      if (a.w_post) {
+      if (has_post) {
         get(stage, kY, i, off).unpack(f);
 #pragma unroll
         for (int e = 0; e < V; ++e) s[2] = fmaf(f[e], f[e], s[2]);
@@ -270,8 +273,8 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
   };
   float r = 0.0f, q = 1.0f, zc = 0.0f;  // d = dz + r (w dh - z zc)
   auto statistics = [&](const float* s) {
-    if (a.dh) r = rsqrtf(s[0] * inv_h + a.eps);
-    if (a.w_post) q = rsqrtf(s[2] * inv_h + a.eps);
+    if (has_dh) r = rsqrtf(s[0] * inv_h + a.eps);
+    if (has_post) q = rsqrtf(s[2] * inv_h + a.eps);
     zc = r * r * (s[1] * inv_h);
   };
   // One barrier per row: the second sum of row t and the first sums of the CTA's next row are joined together.
@@ -300,13 +303,13 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
     for (int i = 0; i < W; ++i) {
       const int v = threadIdx.x + i * nth;
       if (v >= nv) continue;
-      if (a.dz) {
+      if (has_dz) {
         get(stage, kDz, i, off).unpack(d[i]);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) d[i][e] = 0.0f;
       }
-      if (a.dh) {
+      if (has_dh) {
         float zf[V], f[V], w[V];
         get(stage, kZ, i, off).unpack(zf);
         get(stage, kDh, i, off).unpack(f);
@@ -317,17 +320,17 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
           d[i][e] = fmaf(r, w[e] * f[e] - zf[e] * zc, d[i][e]);
         }
       }
-      if (a.dx) store_vec(static_cast<T*>(a.dx) + off, v, Pack<T, V>::of(d[i]));
-      if (!a.y) continue;
+      if (has_dx) store_vec(static_cast<T*>(a.dx) + off, v, Pack<T, V>::of(d[i]));
+      if (!has_y) continue;
       float yf[V], w[V];
       get(stage, kY, i, off).unpack(yf);
-      if (a.w_post) {
+      if (has_post) {
         wp[i].unpack(w);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) w[e] = 1.0f;
       }
-      if (a.gate_full) {
+      if (has_gate) {
         float g[V], dg[V];
         get(stage, kGate, i, off).unpack(g);
 #pragma unroll
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
     if (t + gridDim.x < a.T) first_sums(s, after, off + size_t(gridDim.x) * a.H);
     block_sum<4>(s, ahead ? red2 : red1);
     if (a.dgate_tok && threadIdx.x == 0) a.dgate_tok[t] = a.alpha * dat * q * s[3];
-    if (a.y) {
+    if (has_y) {
       const float c = a.alpha * at;
       const float yc = q * q * (s[3] * inv_h);  // dy = c q (w_post d - y yc)
 #pragma unroll
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
         const int v = threadIdx.x + i * nth;
         if (v >= nv) continue;
         float o[V];
-        if (a.w_post) {
+        if (has_post) {
           float yf[V], w[V];
           get(stage, kY, i, off).unpack(yf);
           wp[i].unpack(w);
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
 #pragma unroll
           for (int e = 0; e < V; ++e) o[e] = c * d[i][e];
         }
-        if (a.dy) store_vec(static_cast<T*>(a.dy) + off, v, Pack<T, V>::of(o));
+        if (has_dy) store_vec(static_cast<T*>(a.dy) + off, v, Pack<T, V>::of(o));
       }
     }
     statistics(s);
@@ -386,8 +389,8 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
     if (v >= nv) continue;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      if (a.w_post) part[size_t(v) * V + e] = gp[i][e];
-      if (a.dh) part[a.H + size_t(v) * V + e] = gn[i][e];
+      if (has_post) part[size_t(v) * V + e] = gp[i][e];
+      if (has_dh) part[a.H + size_t(v) * V + e] = gn[i][e];
     }
   }
 }
@@ -459,8 +462,8 @@ int bwd_grid(int T, int nv) {
 }
 constexpr int kSmemMax = 224 * 1024;
 
-template <typename T, int V, int W, int THREADS, bool DIRECT>
-cudaError_t run_bwd(const NormArgs& a, int grid, cudaStream_t st) {
+template <typename T, int V, int W, int THREADS, bool DIRECT, bool FULL>
+cudaError_t run_bwd_as(const NormArgs& a, int grid, cudaStream_t st) {
   // raised once per device, so no later call (e.g. one inside a stream capture) sets attributes
   static std::atomic<bool> done[128] = {};
   int dev = 0;
@@ -468,14 +471,23 @@ cudaError_t run_bwd(const NormArgs& a, int grid, cudaStream_t st) {
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
   if (!done[dev].load(std::memory_order_acquire)) {
-    err = cudaFuncSetAttribute(k_block_norm_bwd<T, V, W, THREADS, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    err = cudaFuncSetAttribute(k_block_norm_bwd<T, V, W, THREADS, DIRECT, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (err != cudaSuccess) return err;
     done[dev].store(true, std::memory_order_release);
   }
   const int threads = round32((a.H / V + W - 1) / W), stage = bwd_stage_bytes<T, V, W, THREADS>(a.gate_full != nullptr);
   const int depth = DIRECT || 3 * stage > kSmemMax / bwd_ctas(THREADS) ? 2 : 3;
-  k_block_norm_bwd<T, V, W, THREADS, DIRECT><<<unsigned(grid), threads, DIRECT ? 0 : size_t(depth) * stage, st>>>(a, depth);
+  k_block_norm_bwd<T, V, W, THREADS, DIRECT, FULL><<<unsigned(grid), threads, DIRECT ? 0 : size_t(depth) * stage, st>>>(a, depth);
   return cudaGetLastError();
+}
+
+template <typename T, int V, int W, int THREADS, bool DIRECT>
+cudaError_t run_bwd(const NormArgs& a, int grid, cudaStream_t st) {
+  // the usual step of rows that fill vectors gets a kernel of its own: 110 -> 97 us at 4096 x 7168
+  if constexpr (V > 1 && W <= 2) {
+    if (a.dh && a.dz && a.y && a.w_post && a.dx && a.dy && !a.gate_full) return run_bwd_as<T, V, W, THREADS, DIRECT, true>(a, grid, st);
+  }
+  return run_bwd_as<T, V, W, THREADS, DIRECT, false>(a, grid, st);
 }
 
 template <typename T, int V>
