@@ -196,11 +196,22 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route_bwd(const float* __r
 constexpr int kPermThreads = 1024;
 constexpr int kPermCntInts = 8192;  // 32 KiB of counts: NW = min(32, 8192 / (E + 1))
 
+// The bins of kPermAhead pairs p, p + 32, ... (all loads in flight); -1 past the end.
+constexpr int kPermAhead = 4;
+MOE_DEVICE void load_ids(const int32_t* ids, int p, int end, int E, int (&id)[kPermAhead]) {
+#pragma unroll
+  for (int r = 0; r < kPermAhead; ++r) id[r] = p + 32 * r < end ? ids[p + 32 * r] : -2;
+#pragma unroll
+  for (int r = 0; r < kPermAhead; ++r) id[r] = p + 32 * r >= end ? -1 : id[r] >= 0 && id[r] < E ? id[r] : E;
+}
+
+template <int C>
 __global__ void __launch_bounds__(kPermThreads) k_permute_cap(const int32_t* __restrict__ ids, int P, int E, int cap,
-                                                              int NW, int C, moe_routing_t out) {
+                                                              int NW, moe_routing_t out) {
   __shared__ int cnt[kPermCntInts];
   __shared__ int tot[MOE_MAX_EXPERTS + 1];   // this CTA's pairs per bin
-  __shared__ int base[MOE_MAX_EXPERTS + 1];  // pairs of the bin in earlier CTAs, then the first row
+  __shared__ int base[MOE_MAX_EXPERTS + 1];  // pairs of the bin in earlier CTAs
+  __shared__ int first[MOE_MAX_EXPERTS];     // the expert's first row
   __shared__ int dropped[33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwb = blockDim.x >> 5;
   const int B = E + 1;
@@ -211,21 +222,18 @@ __global__ void __launch_bounds__(kPermThreads) k_permute_cap(const int32_t* __r
   const int beg = int(q * P / Q), end = int((q + 1) * P / Q);
   int* mine = cnt + warp * B;
   if (warp < NW) {
-    for (int p0 = beg; p0 < end; p0 += 32) {
-      const int p = p0 + lane;
-      int id = -1;
-      if (p < end) {
-        id = ids[p];
-        id = id >= 0 && id < E ? id : E;
-      }
-      const unsigned peers = __match_any_sync(0xffffffffu, id);
-      if (id >= 0 && (__ffs(peers) - 1) == lane) mine[id] += __popc(peers);
-      __syncwarp();
+    for (int p0 = beg; p0 < end; p0 += 32 * kPermAhead) {
+      int id[kPermAhead];
+      load_ids(ids, p0 + lane, end, E, id);
+#pragma unroll
+      for (int r = 0; r < kPermAhead; ++r)
+        if (id[r] >= 0) atomicAdd(&mine[id[r]], 1);
     }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < B; e += blockDim.x) {
     int run = 0;
+#pragma unroll 8
     for (int w = 0; w < NW; ++w) {
       const int c = cnt[w * B + e];
       cnt[w * B + e] = run;
@@ -242,7 +250,8 @@ __global__ void __launch_bounds__(kPermThreads) k_permute_cap(const int32_t* __r
   int all_of[2] = {0, 0};  // B <= 1025 bins over 1024 threads
   for (int i = 0, e = threadIdx.x; e < B; e += blockDim.x, ++i) {
     int before = 0, all = 0;
-    for (int c = 0; c < C; ++c) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {  // all reads in flight at once
       const int v = C > 1 ? *cg::this_cluster().map_shared_rank(&tot[e], c) : tot[e];
       before += c < rank ? v : 0;
       all += v;
@@ -267,11 +276,7 @@ __global__ void __launch_bounds__(kPermThreads) k_permute_cap(const int32_t* __r
     for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     if (lane == 0) dropped[w] = s;
   }
-  __syncthreads();
-  // cnt: index inside the expert of the warp's next pair; base: first row; dropped[32]: kept rows
-  for (int i = threadIdx.x; i < NW * B; i += blockDim.x) cnt[i] += base[i % B];
-  __syncthreads();
-  if (warp == 0) {
+  if (warp == 0) {  // dropped[32]: kept rows
     const int per = (E + 31) / 32;
     const int b = min(E, lane * per), en = min(E, b + per);
     int sum = 0, act = 0;
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(kPermThreads) k_permute_cap(const int32_t* __r
     int run = isum - sum, pos = iact - act;
     for (int e = b; e < en; ++e) {
       const int n = min(tot[e], limit);
-      base[e] = run;
+      first[e] = run;
       if (rank == 0) {
         out.expert_offsets[e] = run;
         if (n > 0) out.expert_list[1 + pos] = e;
@@ -312,27 +317,27 @@ __global__ void __launch_bounds__(kPermThreads) k_permute_cap(const int32_t* __r
   const int kept_rows = dropped[32];
   int drop_at = kept_rows + dropped[warp];
   const unsigned lt = (1u << lane) - 1u;
-  for (int p0 = beg; p0 < end; p0 += 32) {
-    const int p = p0 + lane;
-    int id = -1;
-    if (p < end) {
-      id = ids[p];
-      id = id >= 0 && id < E ? id : E;
+  for (int p0 = beg; p0 < end; p0 += 32 * kPermAhead) {
+    int ahead[kPermAhead];
+    load_ids(ids, p0 + lane, end, E, ahead);
+#pragma unroll
+    for (int r = 0; r < kPermAhead; ++r) {
+      const int p = p0 + 32 * r + lane, id = ahead[r];
+      const unsigned peers = __match_any_sync(0xffffffffu, id);
+      int idx = 0;
+      if (id >= 0) idx = base[id] + mine[id] + __popc(peers & lt);
+      __syncwarp();
+      if (id >= 0 && (__ffs(peers) - 1) == lane) mine[id] += __popc(peers);
+      __syncwarp();
+      const bool keep = id >= 0 && id < E && idx < limit;
+      const unsigned lost = __ballot_sync(0xffffffffu, id >= 0 && !keep);
+      if (id >= 0) {
+        const int row = keep ? first[id] + idx : drop_at + __popc(lost & lt);
+        out.sorted_pair[row] = p;
+        out.pair_to_row[p] = keep ? row : -1;
+      }
+      drop_at += __popc(lost);
     }
-    const unsigned peers = __match_any_sync(0xffffffffu, id);
-    int idx = 0;
-    if (id >= 0) idx = mine[id] + __popc(peers & lt);
-    __syncwarp();
-    if (id >= 0 && (__ffs(peers) - 1) == lane) mine[id] += __popc(peers);
-    __syncwarp();
-    const bool keep = id >= 0 && id < E && idx < limit;
-    const unsigned lost = __ballot_sync(0xffffffffu, id >= 0 && !keep);
-    if (id >= 0) {
-      const int row = keep ? base[id] + idx : drop_at + __popc(lost & lt);
-      out.sorted_pair[row] = p;
-      out.pair_to_row[p] = keep ? row : -1;
-    }
-    drop_at += __popc(lost);
   }
 }
 
@@ -400,7 +405,7 @@ cudaError_t launch_route_bwd(const float* dw, const float* w, const int32_t* ids
 cudaError_t launch_permute_capacity(const int32_t* ids, int P, int E, int cap, const moe_routing_t& out,
                                     cudaStream_t st) {
   const int most = kPermCntInts / (E + 1) < 32 ? kPermCntInts / (E + 1) : 32;
-  const int C = P > 4096 ? 8 : 1;  // pairs enough for several CTAs
+  const int C = P > 1024 ? 8 : 1;  // pairs enough for several CTAs (4096 pairs: one CTA 12.3, eight 7 us)
   const int want = (P + 32 * C - 1) / (32 * C);
   const int NW = want < most ? want : most;
   // the bins are walked by all threads, two per thread at most
@@ -416,7 +421,8 @@ cudaError_t launch_permute_capacity(const int32_t* ids, int P, int E, int cap, c
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_permute_cap, ids, P, E, cap, NW, C, out);
+  if (C == 1) return cudaLaunchKernelEx(&cfg, k_permute_cap<1>, ids, P, E, cap, NW, out);
+  return cudaLaunchKernelEx(&cfg, k_permute_cap<8>, ids, P, E, cap, NW, out);
 }
 
 }  // namespace moe
