@@ -546,7 +546,7 @@ static moe_status_t check_norm(const moe_block_norm_t* b, moe_dtype_t dt, int64_
   if (!(b->eps > 0.0f) || b->eps > 1e30f || !(b->alpha >= -1e30f && b->alpha <= 1e30f)) return MOE_ERR_INVALID_ARG;
   if (b->gate_mode != MOE_GATE_NONE && b->gate_mode != MOE_GATE_TOKEN && b->gate_mode != MOE_GATE_FULL)
     return MOE_ERR_INVALID_ARG;
-  if (H > 16384 || T > INT_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (H > 16384 || T > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
   if ((b->gate_mode == MOE_GATE_NONE) != (b->gate == nullptr)) return MOE_ERR_INVALID_ARG;
   if (!b->y && (b->w_post || b->gate || b->pair_to_row)) return MOE_ERR_INVALID_ARG;

@@ -476,6 +476,7 @@ moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, cons
  * without a row (dropped: nothing is read or written for it).  w_p = topk_w[p] where `weighted`
  * is nonzero, else 1.  Element types: moe_dtype_t; sums in fp32 in slot order, rounded once.
  * Of the routing only pair_to_row is read (and topk_w where weighted), 4-byte aligned.
+ * Each row belongs to one pair at most (as the permutations write it).
  * Row buffers need only their element's alignment: 128-bit accesses are used when they start on
  * 16 bytes and H is a multiple of 16 bytes, else single elements.  Rows that no pair refers to are
  * left as they are.  1 <= H <= 2^20, 1 <= k <= MOE_MAX_TOPK, T * k <= 2^30.  Outputs must not overlap inputs,
@@ -560,7 +561,7 @@ typedef struct {
 /* z and h of the step above, each rounded once to the element type (h from the unrounded z).
  * z: needed if y is given, else not written (NULL).  h: needed if w_next is given, else NULL.  At
  * least one of the two.  z may be x (in place); no other overlap of outputs with inputs or each other.
- * eps > 0; 1 <= H <= 16384.  Row buffers and weights: their element's alignment (128-bit accesses as
+ * eps > 0; 1 <= H <= 16384; T <= 2^30.  Row buffers and weights: their element's alignment (128-bit accesses as
  * for the calls above); gate per token, pair_to_row and topk_w: 4 bytes.  |y|, |z| < 2^56 keep the
  * sums of squares finite.  Deterministic. */
 moe_status_t moe_block_norm(const moe_block_norm_t* step, const void* x, moe_dtype_t dtype, int64_t T, int64_t H, void* z,

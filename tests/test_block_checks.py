@@ -98,6 +98,7 @@ def test_block_norm(lib):
     assert call(T=-1) == INVALID
     assert call(H=0) == INVALID
     assert call(H=16385) == SHAPE
+    assert call(T=(1 << 30) + 1) == SHAPE
     assert call(eps=0.0) == INVALID
     assert call(eps=float("nan")) == INVALID
     assert call(alpha=float("inf")) == INVALID

@@ -284,3 +284,51 @@ def test_around_the_grouped_ffn(moe, cuda_device, T):
     rf = np.nan_to_num(_f64(rows))
     ref = ro.unsort_rows(rf, _f64(r.topk_w), b, T, k, _f64(x))
     _close(out, ref, ro.unsort_rows(np.abs(rf), _f64(r.topk_w), b, T, k, np.abs(_f64(x))), k + 2, torch.bfloat16, "layer")
+
+
+@pytest.mark.parametrize("T", [3, 300])
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_every_pair_dropped(moe, cuda_device, T, fmt):
+    """A rank none of whose experts were chosen: the grouped FFN computes nothing, every token keeps its residual, and the
+    gradients of the weights are zero."""
+    H, I, E, k = 256, 128, 4, 2
+    x = torch.randn((T, H), generator=torch.Generator().manual_seed(T)).bfloat16().cuda()
+    ex = moe.quantize_experts(fmt, torch.ones((E, 2 * I, H), dtype=torch.bfloat16, device="cuda"),
+                              torch.ones((E, H, I), dtype=torch.bfloat16, device="cuda"))
+    r = moe.moe_permute_capacity(torch.full((T * k,), E, dtype=torch.int32, device="cuda"), T, k, E)
+    r.topk_w = torch.ones(T * k, device="cuda")
+    assert int(r.expert_offsets[E]) == 0 and int(r.expert_list[0]) == 0
+    held = torch.full((T * k, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    rows = moe.moe_grouped_ffn(x, r, ex, I, E, k, bits=torch.full((T * k,), 4, dtype=torch.uint8, device="cuda"), y_rows=held)
+    moe.moe_check_device_errors()
+    assert bool((rows == 7).all())
+    rows.fill_(float("nan"))
+    assert torch.equal(moe.moe_unsort_rows(rows, r, T, k, residual=x), x)
+    assert bool((moe.moe_unsort_rows(rows, r, T, k) == 0).all())
+    dr, dw = moe.moe_unsort_rows_bwd(x, r, k, rows=rows, d_rows=torch.full_like(rows, 3.0))
+    assert bool((dr == 3).all()) and bool((dw == 0).all())
+    z, _ = moe.moe_block_norm(x, rows, routing=r, k=k, w_post=torch.ones(H, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(z, x)
+
+
+def test_two_streams_at_once(moe, cuda_device):
+    """Calls without a workspace on two streams at the same time."""
+    T, H, E, k = 512, 1024, 32, 4
+    cases = [_case(s, T, H, E, k, torch.bfloat16, -2, 32) for s in (21, 22)]
+
+    def chain(c, stream):
+        ids, x, rows, w = c
+        r = moe.moe_permute_capacity(ids, T, k, E, 70, stream=stream)
+        r.topk_w = w
+        out = moe.moe_unsort_rows(rows, r, T, k, residual=x, stream=stream)
+        return out, moe.moe_sort_rows_bwd(rows, r, T, k, x=x, weighted=True, stream=stream)
+
+    ref = [chain(c, None) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = [chain(c, s) for c, s in zip(cases, streams)]
+        for s in streams:
+            s.synchronize()
+        for (a, (b, c)), (p, (q, r)) in zip(got, ref):
+            assert torch.equal(a, p) and torch.equal(b, q) and torch.equal(c, r)
