@@ -25,8 +25,13 @@ cudaError_t launch_linear_w4(const moe_linear_t& w, const void* x, int64_t ldx, 
   a.K = K;
   a.swiglu = act == MOE_ACT_SWIGLU;
   const bool bf16 = x_dtype == MOE_BF16;
-  // UMMA_OVERRIDE
-  if (T > 16) return linear_umma(a, w.fmt, bf16, st);
+  // A tcgen05 pass takes 64 tokens in about the time of one; a pass here takes 16, but in a tenth of the latency, and
+  // several passes fill the machine that a small matrix leaves empty.  The unit is one warp's: 16 rows x 128 k x 16 tokens.
+  // Up to 30000 of them (200 per SM) passes take 0.4 .. 0.95 of tcgen05's time, 1.09 at worst (128 x 2048, 64 tokens: 5.5
+  // against 13.6 us; 512 x 7168: 8.6 against 17.0; 7168 x 2048: 16.0 against 20.3; 4096 x 7168, 20 tokens: 16.7 against
+  // 15.5); at 43000 they take 1.1 .. 1.3 of it (4096 x 7168, 40 tokens: 25.6 against 20.0 us).
+  const int64_t units = int64_t((T + 15) / 16) * ((N + 15) / 16) * (K / 128);
+  if (T > 16 && units > 30000) return linear_umma(a, w.fmt, bf16, st);
   if (w.fmt == MOE_FMT_W4G128)
     return bf16 ? pick_linear<true, MOE_FMT_W4G128>(a, st) : pick_linear<false, MOE_FMT_W4G128>(a, st);
   return linear_nvfp4(a, bf16, st);

@@ -1,6 +1,6 @@
 // Matrix-vector products with 4-bit weights and group scales: y[t][n] = sum_k x[t][k] w[n][k], w one W4G128 or NVFP4
-// matrix as the quantisers write it, SwiGLU or a residual in the epilogue.  This kernel serves up to 16 tokens; more go to
-// the tcgen05 kernel (moe_linear_umma.cuh).
+// matrix as the quantisers write it, SwiGLU or a residual in the epilogue.  This kernel serves up to 16 tokens, and small
+// matrices in passes of 16; the rest goes to the tcgen05 kernel (moe_linear_umma.cuh).
 //
 // Bound by the weight stream (half a byte per weight plus scales): each weight is read once, dequantised in registers, and
 // meets all tokens on mma.sync m16n8k16 (16 weight rows x 16 k x 8 tokens).  A tcgen05 tile would be mostly empty, and its
@@ -50,8 +50,6 @@ struct LinearArgs {
 namespace {
 
 namespace cg = cooperative_groups;
-
-
 
 // The eight W4 codes of a word as q = u - 8, pairs p of nibbles (p, p + 4).  A code is put into the mantissa of a
 // constant whose last place is one unit: bf16 128 + u, fp16 1024 + u; fp16 has room for a nibble four bits up
@@ -227,7 +225,7 @@ __global__ void __launch_bounds__(Lin<NT, KW>::kThreads, Lin<NT, KW>::kCtas) k_l
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int wr = warp / KW, kw = warp % KW;
   const int part = blockIdx.y;  // K part of this CTA (its rank in the cluster)
-  const int t0 = 0, nt = a.T;  // at most 8 NT
+  const int t0 = blockIdx.z * (8 * NT), nt = min(a.T - t0, 8 * NT);  // this pass's tokens
   const int G = a.K / 128;
   const int gb = int(int64_t(part) * G / a.S), ge = int(int64_t(part + 1) * G / a.S);
   const int chunks = (ge - gb + CG - 1) / CG;
@@ -339,9 +337,9 @@ __global__ void __launch_bounds__(Lin<NT, KW>::kThreads, Lin<NT, KW>::kCtas) k_l
       const uint4 wb = *reinterpret_cast<const uint4*>(ring + slot + 512);
       const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
       const uint32_t qa = sa[ii % SR], qb = sb[ii % SR];
-      // The operands of word j; with one tile of tokens all four words are dequantised first (49 against 55 us at
-      // 50304 x 7168, 1 token), with more each word meets its tokens at once, which needs fewer registers (71 against 76 us
-      // with 16 tokens).
+      // The operands of word j; with one tile of tokens all four words are dequantised first (10% less time at
+      // 50304 x 7168, 1 token), with more each word meets its tokens at once, which needs fewer registers (6% less with 16
+      // tokens).
       constexpr int HELD = NT == 1 ? 4 : 1;
       uint32_t pa[HELD][4], pb[HELD][4];
       auto dequantise = [&](int j) {
@@ -389,12 +387,12 @@ __global__ void __launch_bounds__(Lin<NT, KW>::kThreads, Lin<NT, KW>::kCtas) k_l
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (HELD == 1) dequantise(j);
-        const uint32_t(&qa_)[4] = pa[j % HELD], (&qb_)[4] = pb[j % HELD];
+        const uint32_t(&ra)[4] = pa[j % HELD], (&rb)[4] = pb[j % HELD];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const uint4 b = *reinterpret_cast<const uint4*>(xs + n * 8 * STRIDE + ii * (KW * 256) + j * 64);
-          mma16<BF16>(d[n], qa_[0], qb_[0], qa_[1], qb_[1], b.x, b.y);
-          mma16<BF16>(d[n], qa_[2], qb_[2], qa_[3], qb_[3], b.z, b.w);
+          mma16<BF16>(d[n], ra[0], rb[0], ra[1], rb[1], b.x, b.y);
+          mma16<BF16>(d[n], ra[2], rb[2], ra[3], rb[3], b.z, b.w);
         }
       }
       const float fa = VS ? scale_of(va, ii) : W4 ? __uint_as_float(qa << 16) : 1.0f;
@@ -441,7 +439,7 @@ cudaError_t run_linear(const LinearArgs& a, cudaStream_t st) {
   }
   const int tiles = (a.N + 15) / 16;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((tiles + L::kRW - 1) / L::kRW), unsigned(a.S));
+  cfg.gridDim = dim3(unsigned((tiles + L::kRW - 1) / L::kRW), unsigned(a.S), unsigned((a.T + 8 * NT - 1) / (8 * NT)));
   cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = st;
@@ -457,7 +455,7 @@ cudaError_t run_linear(const LinearArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Where K is split (up to 16 tokens): warps on the same rows (KW), then CTAs of a cluster (S).  The machine wants at least a
+// Where K is split: warps on the same rows (KW), then CTAs of a cluster (S).  The machine wants at least a
 // hundred CTAs, and rows that share their staged tokens want to be many per CTA.  Up to 2048 k the warps of a CTA split a
 // group each before a cluster does (joining a cluster costs about 0.4 us); longer rows leave the warps longer runs when the
 // cluster splits first.  Measured at 512 .. 50304 rows of 2048 .. 7168 k; against the best of all splits at most 8% slower.
@@ -465,7 +463,8 @@ template <bool BF16, int FMT>
 cudaError_t pick_linear(LinearArgs a, cudaStream_t st) {
   const int NT = a.T <= 8 ? 1 : 2, kw_most = NT == 1 ? 8 : 4;
   const int tiles = (a.N + 15) / 16, G = a.K / 128, enough = 100;
-  auto blocks = [&](int kw) { return (tiles + 8 / kw - 1) / (8 / kw); };
+  const int passes = (a.T + 15) / 16;
+  auto blocks = [&](int kw) { return (tiles + 8 / kw - 1) / (8 / kw) * passes; };
   int KW = 1, S = 1;
   if (G <= 16) {
     while (KW < kw_most && blocks(KW) < enough && KW * 2 <= G) KW *= 2;
@@ -476,7 +475,6 @@ cudaError_t pick_linear(LinearArgs a, cudaStream_t st) {
     while (S < 4 && blocks(KW) * S * 2 <= most) S *= 2;
   }
   a.S = S;
-  // LIN_OVERRIDE
   // every part of K starts a chunk's scales on a vector's boundary
   constexpr bool W4 = FMT == MOE_FMT_W4G128;
   const int chunk = NT == 1 ? 8 : 4;

@@ -37,19 +37,15 @@ cudaError_t encode_tokens(CUtensorMap* map, const LinearArgs& a, bool bf16, int 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Parts of K: as many CTAs as SMs, as long as each set keeps a group or more; with a block of rows for every other SM the
-// split costs more than it gives (4096 x 7168, 64 tokens: 4 parts 23.6, 2 parts 30 us; 12288 x 4096: 1 part 31.7, 2 parts
+// Parts of K: as many CTAs as SMs (a call with few blocks has many groups: it would not come here otherwise); with a block
+// of rows for every other SM the split costs more than it gives (4096 x 7168, 64 tokens: 4 parts 23.6, 2 parts 30 us; 12288 x 4096: 1 part 31.7, 2 parts
 // 36 us).  Six rather than eight where eight would not fill the machine either (2048 x 7168: 20.5 against 25.7 us).
-int umma_parts(int blocks, int G) {
-  const int S = blocks > 73 ? 1 : blocks > 36 ? 2 : blocks > 18 ? 4 : blocks > 9 ? 6 : 8;
-  return S * 2 <= G ? S : G >= 2 ? G / 2 : 1;
-}
+int umma_parts(int blocks) { return blocks > 73 ? 1 : blocks > 36 ? 2 : blocks > 18 ? 4 : blocks > 9 ? 6 : 8; }
 
 template <bool BF16, int FMT>
 cudaError_t pick_umma(LinearArgs a, unsigned* err, cudaStream_t st) {
   const int rows = a.swiglu ? (a.N / 2 + 63) / 64 : (a.N + 127) / 128, passes = (a.T + kPassTokens - 1) / kPassTokens;
-  a.S = umma_parts(rows > 1000 || passes > 1000 ? 1000 : rows * passes, a.K / 128);
-  // UMMA_S
+  a.S = umma_parts(rows > 1000 || passes > 1000 ? 1000 : rows * passes);
   return a.T <= 32 ? run_umma<BF16, FMT, 32>(a, err, st) : run_umma<BF16, FMT, 64>(a, err, st);
 }
 

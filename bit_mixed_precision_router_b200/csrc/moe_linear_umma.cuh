@@ -1,4 +1,4 @@
-// moe_linear_w4 on the fifth-generation tensor cores, for more than 16 tokens.
+// moe_linear_w4 on the fifth-generation tensor cores, for more than 16 tokens of a larger matrix.
 //
 // A CTA owns 128 weight rows (the lanes of tensor memory, MMA M) and one part of K; the tokens are MMA N = 32 or 64, larger
 // batches take passes of 64.  Roles:

@@ -81,6 +81,51 @@ def test_swiglu_and_residual(moe, cuda_device, T, N, K, fmt, residual):
         _check(got, x, w, act == moe.ACT_SWIGLU, None if res is None else _f64(res))
 
 
+# More than 16 tokens and more than 30000 units of 16 rows x 128 k x 16 tokens: the tcgen05 kernel.  One pass of 32 or 64
+# tokens and several, ragged ends of each; K in 1, 2, 4, 6 and 8 parts; one, two and odd numbers of groups
+LARGE = [(17, 4100, 7680), (32, 15500, 2048), (33, 5411, 3968), (64, 17000, 1024), (65, 33000, 384), (130, 27001, 256), (300, 515, 7168),
+         (1000, 7700, 128), (4100, 34, 5248), (64, 2048, 7680), (64, 1152, 13568)]
+
+
+def _is_large(T, N, K):
+    return T > 16 and -(-T // 16) * -(-N // 16) * (K // 128) > 30000
+
+
+@pytest.mark.parametrize("T,N,K", LARGE)
+@pytest.mark.parametrize("fmt,xt,yt", [(0, "bf16", "bf16"), (0, "f16", "f32"), (2, "bf16", "f32"), (2, "f16", "f16")])
+def test_product_of_larger_ones(moe, cuda_device, T, N, K, fmt, xt, yt):
+    assert _is_large(T, N, K)
+    lin, w = _matrix(moe, fmt, N, K, N + K)
+    x = torch.randn((T, K), generator=torch.Generator().manual_seed(T)).to(DT[xt]).cuda()
+    got = moe.moe_linear_w4(x, lin, out_dtype=DT[yt])
+    _check(got, x, w, False, None)
+    assert torch.equal(got, moe.moe_linear_w4(x, lin, out_dtype=DT[yt]))
+    moe.moe_check_device_errors()
+
+
+@pytest.mark.parametrize("T,N,K", [(20, 7778, 4096), (33, 5402, 3968), (200, 1026, 4736), (4100, 34, 5248)])
+@pytest.mark.parametrize("fmt", [0, 2])
+@pytest.mark.parametrize("residual", [None, "rows", "bias"])
+def test_swiglu_and_residual_of_larger_ones(moe, cuda_device, T, N, K, fmt, residual):
+    assert _is_large(T, N, K)
+    test_swiglu_and_residual(moe, cuda_device, T, N, K, fmt, residual)
+
+
+@pytest.mark.parametrize("T,N,K", [(40, 50, 256), (40, 6001, 3584)])  # passes of 16 tokens, and tcgen05
+def test_strided_rows_of_many_tokens(moe, cuda_device, T, N, K):
+    assert _is_large(T, N, K) == (N > 1000)
+    lin, _ = _matrix(moe, 0, N, K, 1)
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn((T, K + 24), generator=g).bfloat16().cuda()[:, 8:8 + K]
+    res = torch.randn((T, N), generator=g).bfloat16().cuda()
+    ref = moe.moe_linear_w4(x.contiguous(), lin, residual=res)
+    buf = torch.full((T + 1, N + 13), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = moe.moe_linear_w4(x, lin, residual=res, out=buf[:T, 5:5 + N])
+    assert torch.equal(got, ref)
+    assert bool((buf[:, :5] == 7).all()) and bool((buf[:, 5 + N:] == 7).all()) and bool((buf[T] == 7).all())
+    assert torch.equal(moe.moe_linear_w4(x, lin, residual=res, out=res), ref)  # in place
+
+
 def test_strided_rows_and_in_place_residual(moe, cuda_device):
     """Rows inside wider buffers; what lies between them is not touched."""
     T, N, K = 6, 50, 256
@@ -109,10 +154,10 @@ def test_large_and_tiny_tokens(moe, cuda_device):
     _check(moe.moe_linear_w4(x, lin), x, w, False, None)
 
 
-@pytest.mark.parametrize("T", [3, 12, 40])
-def test_infinities_and_nan_stay_in_their_token(moe, cuda_device, T):
-    lin, w = _matrix(moe, 2, 70, 256, 7)
-    x = torch.randn((T, 256), generator=torch.Generator().manual_seed(8)).bfloat16().cuda()
+@pytest.mark.parametrize("T,N,K", [(3, 70, 256), (12, 70, 256), (40, 70, 256), (330, 1500, 2048)])
+def test_infinities_and_nan_stay_in_their_token(moe, cuda_device, T, N, K):
+    lin, w = _matrix(moe, 2, N, K, 7)
+    x = torch.randn((T, K), generator=torch.Generator().manual_seed(8)).bfloat16().cuda()
     ref = moe.moe_linear_w4(x, lin)
     x[1, 3], x[2, 100] = float("nan"), float("inf")
     got = moe.moe_linear_w4(x, lin)
