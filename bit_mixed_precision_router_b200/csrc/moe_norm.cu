@@ -4,17 +4,20 @@
 //   n = y rsqrt(mean y^2 + eps) w_post        (n = y without w_post)
 //   z = x + alpha a n,   h = z rsqrt(mean z^2 + eps) w_next
 // One CTA holds one row in registers, so each input is read once and z, h written once; the row
-// sums (two at most, dependent) are CTA reductions in fp32.  Bound by HBM.
+// sums (two at most, dependent) are CTA reductions in fp32.  Bound by HBM (4096 x 7168 bf16: 48 us, 36 us at the copy's rate);
+// with an elementwise gate by half by its sigmoids.
 // Backward, from z, y and the gate (the statistics are recomputed from the row, which is read
 // anyway; nothing is saved by the forward pass), with r = rsqrt(mean z^2 + eps), q = rsqrt(mean y^2 + eps):
 //   d = dz + r (w_next dh) - z r^3 <z, w_next dh> / H                       (the gradient of x)
 //   dn = alpha a d;  dy = q (w_post dn) - y q^3 <y, w_post dn> / H;  dgate = alpha a' d n
 //   dw_next = sum_t dh z r,  dw_post = sum_t dn y q
+// 4096 x 7168 bf16, gate per token: 76 us, 54 us at the copy's rate.
 // A persistent grid: each CTA walks rows t = b, b + gridDim.x, ... with its columns fixed per
 // thread, so the weight gradients accumulate in registers (fp32) and each CTA writes one partial row;
 // a second kernel adds the partial rows in CTA order (no atomics: the result does not depend on timing).
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "moe_internal.h"
 #include "moe_vec.cuh"
@@ -38,13 +41,33 @@ struct NormArgs {
 
 constexpr int kNormSlots = 8;  // routed rows in flight per thread
 
-// __fdividef: within 2 units of the last place for denominators below 2^126, 0 above (where the quotient is below 2^-126)
-MOE_DEVICE float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+// exp(v) and 1 / v for a sigmoid.  __fdividef is within 2 units of the last place below 2^126 and gives 0 above.  Of an
+// elementwise gate of 16 bits the approximations do: exp is off by (2 + 1.2 |v|) 2^-24 relative, far below the result's half step,
+// and values below 2^-126 become 0; a third of the instructions (2048 x 7168 with such a gate: 32.5 -> 30.4 us).
+template <typename T>
+MOE_DEVICE float exp_of(float v) {
+  if constexpr (sizeof(T) == 4) return expf(v);
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * 1.4426950408889634f));
+  return e;
+}
+template <typename T>
+MOE_DEVICE float inverse_of(float v) {
+  if constexpr (sizeof(T) == 4) return __fdividef(1.0f, v);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+template <typename T>
+MOE_DEVICE float sigmoid_of(float v) {
+  return inverse_of<T>(1.0f + exp_of<T>(-v));
+}
 
 // The sigmoid and its derivative without the cancellation of a (1 - a): with e = exp(-|v|) <= 1,
 // sigmoid(|v|) = 1 / (1 + e), sigmoid(-|v|) = e / (1 + e) and the derivative e / (1 + e)^2.
+template <typename T>
 MOE_DEVICE void sigmoid_grad(const float v, float& a, float& da) {
-  const float e = expf(-fabsf(v)), s = __fdividef(1.0f, 1.0f + e);
+  const float e = exp_of<T>(-fabsf(v)), s = inverse_of<T>(1.0f + e);
   a = v >= 0.0f ? s : e * s;
   da = e * s * s;
 }
@@ -59,6 +82,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_block_norm(NormArgs a) {
   const float inv_h = 1.0f / float(a.H);
   Pack<T, V> xp[W], gp[W];
   float y[W][V];
+  const float gate = a.gate_tok ? a.gate_tok[t] : 1.0f;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
@@ -114,7 +138,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_block_norm(NormArgs a) {
       }
     }
     float scale = a.alpha;
-    if (a.gate_tok) scale *= a.sigmoid ? sigmoid(a.gate_tok[t]) : a.gate_tok[t];
+    if (a.gate_tok) scale *= a.sigmoid ? sigmoid_of<float>(gate) : gate;
     if (a.w_post) {
       float s[1] = {0.0f};
 #pragma unroll
@@ -140,7 +164,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_block_norm(NormArgs a) {
         float g[V];
         gp[i].unpack(g);
 #pragma unroll
-        for (int e = 0; e < V; ++e) m[e] *= a.sigmoid ? sigmoid(g[e]) : g[e];
+        for (int e = 0; e < V; ++e) m[e] *= a.sigmoid ? sigmoid_of<T>(g[e]) : g[e];
       }
       xp[i].unpack(xf);
 #pragma unroll
@@ -177,6 +201,8 @@ template <typename T, int V>
 MOE_DEVICE void copy_vec(Pack<T, V>* dst, const T* row, int v) {
   if constexpr (sizeof(Pack<T, V>) == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(row + size_t(v) * V) : "memory");
+  else if constexpr (sizeof(Pack<T, V>) == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(row + size_t(v) * V) : "memory");
   else
     *dst = load_vec<T, V>(row, v);
 }
@@ -235,6 +261,40 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // Single 16-bit elements have no asynchronous copy: a row ahead waits in registers, from the start of one row's work to its
+  // end (while there are registers).
+  constexpr bool HOLD = !DIRECT && sizeof(Pack<T, V>) == 2 && W <= 4;
+  Pack<T, V> held[HOLD ? kArrays : 1][W];
+  auto hold = [&](int t) {
+    if (t >= a.T) return;
+    const size_t off = size_t(t) * a.H;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int v = threadIdx.x + i * nth;
+      if (v >= nv) continue;
+      if (has_dh) {
+        held[kZ][i] = load_vec<T, V>(static_cast<const T*>(a.x) + off, v);
+        held[kDh][i] = load_vec<T, V>(static_cast<const T*>(a.dh) + off, v);
+      }
+      if (has_dz) held[kDz][i] = load_vec<T, V>(static_cast<const T*>(a.dz) + off, v);
+      if (has_y) held[kY][i] = load_vec<T, V>(static_cast<const T*>(a.y) + off, v);
+      if (has_gate) held[kGate][i] = load_vec<T, V>(static_cast<const T*>(a.gate_full) + off, v);
+    }
+  };
+  auto put = [&](int t, int stage) {
+    if (t >= a.T) return;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (threadIdx.x + i * nth >= nv) continue;
+      if (has_dh) {
+        *slot(stage, kZ, i) = held[kZ][i];
+        *slot(stage, kDh, i) = held[kDh][i];
+      }
+      if (has_dz) *slot(stage, kDz, i) = held[kDz][i];
+      if (has_y) *slot(stage, kY, i) = held[kY][i];
+      if (has_gate) *slot(stage, kGate, i) = held[kGate][i];
+    }
+  };
   Pack<T, V> wn[W], wp[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) {
@@ -279,6 +339,8 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
   };
   // One barrier per row: the second sum of row t and the first sums of the CTA's next row are joined together.
   int stage = 0, ahead = 1;
+  // the gate of the next row, read a row ahead: reading it in its own row cost a fifth of the time (97 against 76 us)
+  float gate = a.gate_tok ? a.gate_tok[blockIdx.x] : 1.0f;
   fetch(blockIdx.x, 0);
   fetch(blockIdx.x + gridDim.x, 1);
   asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -290,12 +352,15 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
   }
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, ahead ^= 1) {
     const int after = stage + 1 == depth ? 0 : stage + 1;  // the next row's stage
-    if (depth == 3) fetch(t + 2 * gridDim.x, after + 1 == depth ? 0 : after + 1);
+    if constexpr (HOLD)
+      hold(t + 2 * gridDim.x);
+    else if (depth == 3)
+      fetch(t + 2 * gridDim.x, after + 1 == depth ? 0 : after + 1);
     const size_t off = size_t(t) * a.H;
-    float at = 1.0f, dat = 1.0f;  // the token's gate and its derivative
+    float at = gate, dat = 1.0f;  // the token's gate and its derivative
     if (a.gate_tok) {
-      at = a.gate_tok[t];
-      if (a.sigmoid) sigmoid_grad(at, at, dat);
+      if (t + gridDim.x < a.T) gate = a.gate_tok[t + gridDim.x];
+      if (a.sigmoid) sigmoid_grad<float>(at, at, dat);
     }
     float d[W][V];
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // [3]: <y, w_post d> (with the elementwise gate: <y, w_post a d>)
@@ -336,7 +401,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           float c = g[e], dc = 1.0f;
-          if (a.sigmoid) sigmoid_grad(g[e], c, dc);
+          if (a.sigmoid) sigmoid_grad<T>(g[e], c, dc);
           dg[e] = a.alpha * dc * d[i][e] * (yf[e] * q * w[e]);
           d[i][e] *= c;
         }
@@ -378,7 +443,10 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
       }
     }
     statistics(s);
-    if (depth == 2) fetch(t + 2 * gridDim.x, stage);
+    if constexpr (HOLD)
+      put(t + 2 * gridDim.x, depth == 2 ? stage : after + 1 == depth ? 0 : after + 1);
+    else if (depth == 2)
+      fetch(t + 2 * gridDim.x, stage);
     stage = after;
   }
   // partial rows: [gridDim.x][2][H]
@@ -404,6 +472,7 @@ __global__ void __launch_bounds__(1024) k_norm_weight_sum(const float* __restric
   if (!out) return;
   float v = 0.0f;
   if (c < H)
+#pragma unroll 8
     for (int g = g0; g < G; g += 32) v += part[(size_t(g) * 2 + blockIdx.y) * H + c];
   s[g0][threadIdx.x & 31] = v;
   __syncthreads();
@@ -446,6 +515,8 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
     k_block_norm<T, V, 2, 512, 2, ROUTED><<<rows, round32((nv + 1) / 2), 0, st>>>(a);
   else if (nv <= 4096)
     k_block_norm<T, V, 4, V == 8 ? 512 : 1024, 1, ROUTED><<<rows, round32((nv + 3) / 4), 0, st>>>(a);
+  else if (V == 1 && nv <= 8192)
+    k_block_norm<T, V, 8, 1024, 1, ROUTED><<<rows, round32((nv + 7) / 8), 0, st>>>(a);
   else if constexpr (V == 1)
     k_block_norm<T, V, 16, 1024, 1, ROUTED><<<rows, round32((nv + 15) / 16), 0, st>>>(a);
   else
@@ -453,11 +524,8 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// The thread count a backward row's kernel is built for (one vector per thread up to 512 vectors, two up to 1024, four or
-// sixteen beyond), and the grid.
-int bwd_threads(int nv) { return nv <= 128 ? 128 : nv <= 256 ? 256 : nv <= 1024 ? 512 : 1024; }
-int bwd_grid(int T, int nv) {
-  const int grid = kSms * bwd_ctas(bwd_threads(nv));
+int bwd_grid(int T, int threads) {
+  const int grid = kSms * bwd_ctas(threads);
   return T < grid ? T : grid;
 }
 constexpr int kSmemMax = 224 * 1024;
@@ -483,32 +551,49 @@ cudaError_t run_bwd_as(const NormArgs& a, int grid, cudaStream_t st) {
 
 template <typename T, int V, int W, int THREADS, bool DIRECT>
 cudaError_t run_bwd(const NormArgs& a, int grid, cudaStream_t st) {
-  // the usual step of rows that fill vectors gets a kernel of its own: 110 -> 97 us at 4096 x 7168
+  // the usual step of rows that fill vectors gets a kernel of its own: 12% less time at 4096 x 7168
   if constexpr (V > 1 && W <= 2) {
     if (a.dh && a.dz && a.y && a.w_post && a.dx && a.dy && !a.gate_full) return run_bwd_as<T, V, W, THREADS, DIRECT, true>(a, grid, st);
   }
   return run_bwd_as<T, V, W, THREADS, DIRECT, false>(a, grid, st);
 }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 template <typename T, int V>
 cudaError_t norm_bwd(const NormArgs& a, int* grid, cudaStream_t st) {
-  const int nv = a.H / V, g = bwd_grid(a.T, nv);
-  *grid = g;
-  if (nv <= 128) return run_bwd<T, V, 1, 128, false>(a, g, st);
-  if (nv <= 256) return run_bwd<T, V, 1, 256, false>(a, g, st);
-  if (nv <= 512) return run_bwd<T, V, 1, 512, false>(a, g, st);
-  if (nv <= 1024) return run_bwd<T, V, 2, 512, false>(a, g, st);
-  // H <= 16384: at most 512 threads of four 8-element vectors, 1024 of narrower ones
-  constexpr int most = V == 8 ? 512 : 1024;
-  if (nv <= 4096) {
-    if (2 * bwd_stage_bytes<T, V, 4, most>(a.gate_full != nullptr) > kSmemMax) return run_bwd<T, V, 4, most, true>(a, g, st);
-    return run_bwd<T, V, 4, most, false>(a, g, st);
+  const int nv = a.H / V;
+  // as many CTAs as run at once for the thread count that the kernel is built for
+  auto run = [&](auto w, auto threads, auto direct) {
+    *grid = bwd_grid(a.T, threads.value);
+    return run_bwd<T, V, w.value, threads.value, direct.value>(a, *grid, st);
+  };
+  constexpr std::false_type staged;
+  constexpr std::true_type direct;
+  if (nv <= 128) return run(Int<1>(), Int<128>(), staged);
+  if (nv <= 256) return run(Int<1>(), Int<256>(), staged);
+  if constexpr (V > 1) {
+    if (nv <= 512) return run(Int<1>(), Int<512>(), staged);
+    if (nv <= 1024) return run(Int<2>(), Int<512>(), staged);
+    // Rows too long for two stages in shared memory are read directly: two stages of 1792 vectors fit (four arrays), of 1024
+    // threads' two no longer.  Two vectors per thread and more threads rather than four of 512 or 1024, which spill (4096 x
+    // 7168 fp32 118 against 340 us, 1000 x 9216 bf16 67 against 101 us).
+    if constexpr (V == 4) {
+      if (nv <= 1792 && !a.gate_full) return run(Int<2>(), Int<896>(), staged);
+    }
+    if (nv <= 2048) return run(Int<2>(), Int<1024>(), direct);
+    if constexpr (V == 4) return run(Int<4>(), Int<1024>(), direct);
+    return cudaErrorInvalidValue;  // H <= 16384: at most 2048 vectors of eight
+  } else {
+    // single elements: four per thread, so that several rows share an SM (4000 x 1001 bf16: 43 us, two of 512 threads 52)
+    if (nv <= 512) return run(Int<4>(), Int<128>(), staged);
+    if (nv <= 1024) return run(Int<4>(), Int<256>(), staged);
+    if (nv <= 2048) return run(Int<4>(), Int<512>(), staged);
+    if (nv <= 4096) return run(Int<4>(), Int<1024>(), staged);
+    if (nv <= 8192) return run(Int<8>(), Int<1024>(), std::bool_constant<sizeof(T) == 4>());
+    return run(Int<16>(), Int<1024>(), direct);
   }
-  if constexpr (V == 1) {
-    if (2 * bwd_stage_bytes<T, V, 16, 1024>(a.gate_full != nullptr) > kSmemMax) return run_bwd<T, V, 16, 1024, true>(a, g, st);
-    return run_bwd<T, V, 16, 1024, false>(a, g, st);
-  }
-  return cudaErrorInvalidValue;
 }
 
 // grid NULL: forward; else backward, and the number of partial rows is stored there
@@ -540,10 +625,12 @@ cudaError_t launch_block_norm(const moe_block_norm_t& b, const void* x, int T, i
   return norm_any(a, dt, nullptr, st);
 }
 
-// the largest grid over the element types and alignments: the fewer vectors a row has, the more CTAs
+// The largest grid over the element types and alignments: the fewest threads that a row can have, an eighth of its length
+// (rows of single elements have a quarter, 128 at least).
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H) {
-  const int t = T < INT_MAX ? int(T) : INT_MAX, h = H < 16384 ? int(H) : 16384;
-  return size_t(bwd_grid(t, (h + 7) / 8)) * 2 * size_t(H) * sizeof(float);
+  const int t = T < INT_MAX ? int(T) : INT_MAX;
+  const int threads = H <= 1024 ? 128 : H <= 2048 ? 256 : 512;
+  return size_t(bwd_grid(t, threads)) * 2 * size_t(H) * sizeof(float);
 }
 
 cudaError_t launch_block_norm_bwd(const moe_block_norm_t& b, const void* z, const void* dz, const void* dh, int T, int H,

@@ -123,6 +123,28 @@ def test_step_and_gradient(moe, cuda_device, T, H, gate, sigmoid, post, nxt, alp
         _check_backward(g, d, zf, y, sigmoid, alpha, dt, False, True)
 
 
+# several rows per CTA of every form of the backward kernel: single elements (one, four, eight and sixteen to a thread),
+# vectors (one, two and four), staged and read directly, with and without the elementwise gate's array
+@pytest.mark.parametrize("T,H,gate,dt", [
+    (2000, 101, "token", "bf16"), (1000, 203, "full", "f16"), (2001, 401, "token", "f16"), (1000, 777, "full", "bf16"),
+    (470, 1501, "token", "f32"), (470, 1999, "full", "bf16"), (450, 3001, "full", "f32"), (450, 3003, "token", "bf16"),
+    (400, 5001, "full", "bf16"), (400, 5001, "token", "f32"), (300, 9001, "token", "f16"), (1000, 2048, "token", "bf16"),
+    (450, 4096, "full", "f16"), (450, 5504, "token", "bf16"), (450, 5504, "full", "bf16"), (450, 5504, "token", "f32"),
+    (450, 7168, "token", "f32"), (320, 7168, "full", "f32"), (320, 8192, None, "f32"), (320, 9216, "token", "bf16"),
+    (320, 9216, "full", "f16"), (300, 12288, "token", "f32")])
+def test_gradient_of_many_rows(moe, cuda_device, T, H, gate, dt):
+    dt = DT[dt]
+    d = _inputs(T + H, T, H, dt, gate, True, True)
+    kw = dict(w_post=d["w_post"], gate=d["gate"], gate_sigmoid=True, alpha=0.5, w_next=d["w_next"], eps=EPS)
+    z, _ = moe.moe_block_norm(d["x"], d["y"], **kw)
+    g = moe.moe_block_norm_bwd(z, d["dz"], d["dh"], y=d["y"], **kw)
+    _check_backward(g, d, _f64(z), _f64(d["y"]), True, 0.5, dt)
+    again = moe.moe_block_norm_bwd(z, d["dz"], d["dh"], y=d["y"], **kw)
+    for f in ("dx", "dy", "dgate", "dw_post", "dw_next"):
+        a, b = getattr(g, f), getattr(again, f)
+        assert (a is None and b is None) or torch.equal(a, b), f
+
+
 @pytest.mark.parametrize("T,H,dt", [(1, 2048, "bf16"), (130, 513, "f32"), (6, 64, "f16"), (700, 128, "bf16")])
 def test_norm_alone(moe, cuda_device, T, H, dt):
     dt = DT[dt]
