@@ -524,9 +524,13 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-int bwd_grid(int T, int threads) {
-  const int grid = kSms * bwd_ctas(threads);
-  return T < grid ? T : grid;
+// CTAs: one or more per SM.  A CTA's rows follow one another, and its partial sums cost 8 H bytes written and read, so their
+// number goes with sqrt(T / H); single elements take longer over a row.  512 x 2048 bf16: 148 CTAs 11.5, 444 CTAs 16.1 us;
+// 4096 x 2048: 148, 296 and 444 CTAs 35, 29 and 32 us; 4000 x 511: 444 and 888 CTAs 35 and 25 us.
+int bwd_grid(int T, int H, int threads, bool single) {
+  int c = 1;
+  while (c < bwd_ctas(threads) && int64_t(2 * c + 1) * (2 * c + 1) * H <= int64_t(single ? 36 : 12) * T) ++c;
+  return T < kSms * c ? T : kSms * c;
 }
 constexpr int kSmemMax = 224 * 1024;
 
@@ -564,9 +568,8 @@ using Int = std::integral_constant<int, N>;
 template <typename T, int V>
 cudaError_t norm_bwd(const NormArgs& a, int* grid, cudaStream_t st) {
   const int nv = a.H / V;
-  // as many CTAs as run at once for the thread count that the kernel is built for
   auto run = [&](auto w, auto threads, auto direct) {
-    *grid = bwd_grid(a.T, threads.value);
+    *grid = bwd_grid(a.T, a.H, threads.value, V == 1);
     return run_bwd<T, V, w.value, threads.value, direct.value>(a, *grid, st);
   };
   constexpr std::false_type staged;
@@ -630,7 +633,7 @@ cudaError_t launch_block_norm(const moe_block_norm_t& b, const void* x, int T, i
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H) {
   const int t = T < INT_MAX ? int(T) : INT_MAX;
   const int threads = H <= 1024 ? 128 : H <= 2048 ? 256 : 512;
-  return size_t(bwd_grid(t, threads)) * 2 * size_t(H) * sizeof(float);
+  return size_t(bwd_grid(t, int(H < 16384 ? H : 16384), threads, true)) * 2 * size_t(H) * sizeof(float);
 }
 
 cudaError_t launch_block_norm_bwd(const moe_block_norm_t& b, const void* z, const void* dz, const void* dh, int T, int H,
