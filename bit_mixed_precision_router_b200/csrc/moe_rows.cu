@@ -24,6 +24,12 @@ namespace cg = cooperative_groups;
 
 constexpr int kRowThreads = 256;
 constexpr int kSlots = 8;  // rows of a token in flight per thread
+// Vectors of a row in flight per thread, of V elements each: with few rows per token, or single elements, a thread takes
+// several (one row per token, 4096 x 4096 bf16: sort 15.7 -> 9.7 us; 4 x 2048 x 2047: 25 -> 13, back 32 -> 17.5).
+// With eight single elements and their dots the registers run out (511 to 8191 of them, back's gradient: 20% to 50% slower).
+__host__ __device__ constexpr int vectors_of(int V, int slots, bool dots) {
+  return slots <= 2 ? 4 : V == 1 && slots <= 4 ? 4 : slots <= 4 ? 2 : V == 1 && slots <= kSlots && !dots ? 4 : 1;
+}
 
 // Sums of N values over the CTA (at most kRowThreads threads), in one fixed order; value j is returned to thread j < N.
 // `red`: 8 N floats of shared memory.
@@ -41,68 +47,78 @@ MOE_DEVICE float block_sums(float (&v)[N], float* red) {
   return s;
 }
 
-template <typename T, int V, bool DOT>
-__global__ void __launch_bounds__(kRowThreads, DOT ? 3 : 0) k_spread(const T* a, const T* __restrict__ b, const float* __restrict__ w,
-                                                        const int32_t* __restrict__ p2r, int H, int k,
-                                                        T* __restrict__ rows, float* __restrict__ dw) {
-  __shared__ float red[kSlots * 8];
+// KB: slots unrolled (k_spread: at a time; k_gather: all, k <= KB).
+template <typename T, int V, bool DOT, int KB>
+__global__ void __launch_bounds__(kRowThreads, DOT ? 3 : 0)
+    k_spread(const T* a, const T* __restrict__ b, const float* __restrict__ w, const int32_t* __restrict__ p2r, int H, int k,
+             T* __restrict__ rows, float* __restrict__ dw) {
+  constexpr int U = vectors_of(V, KB, DOT);
+  __shared__ float red[KB * 8];
   const int t = blockIdx.x, nv = H / V;
   const T* arow = a + size_t(t) * H;
   const int step = DOT ? int(blockDim.x) : int(blockDim.x * gridDim.y);
   const int v0 = DOT ? int(threadIdx.x) : int(blockIdx.y * blockDim.x + threadIdx.x);
-  for (int j0 = 0; j0 < k; j0 += kSlots) {
-    int row[kSlots];
-    float wj[kSlots], dot[kSlots];
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    int row[KB];
+    float wj[KB], dot[KB];
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+    for (int j = 0; j < KB; ++j) {
       const size_t p = size_t(t) * k + j0 + j;
       row[j] = j0 + j < k ? p2r[p] : -1;
       wj[j] = w && j0 + j < k ? w[p] : 1.0f;
       dot[j] = 0.0f;
     }
-    for (int v = v0; v < nv; v += step) {
-      Pack<T, V> bv[kSlots];
-      const Pack<T, V> av = load_vec<T, V>(arow, v);
-      if (DOT) {
+    for (int v = v0; v < nv; v += U * step) {
+      Pack<T, V> av[U], bv[U][KB];
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j)
-          if (row[j] >= 0) bv[j] = load_vec_once<T, V>(b + size_t(row[j]) * H, v);
-      }
-      float f[V];
-      av.unpack(f);
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        if (row[j] < 0) continue;
+      for (int u = 0; u < U; ++u) {
+        if (v + u * step >= nv) break;
+        av[u] = load_vec<T, V>(arow, v + u * step);
         if (DOT) {
-          float g[V];
-          bv[j].unpack(g);
 #pragma unroll
-          for (int i = 0; i < V; ++i) dot[j] = fmaf(f[i], g[i], dot[j]);
+          for (int j = 0; j < KB; ++j)
+            if (row[j] >= 0) bv[u][j] = load_vec_once<T, V>(b + size_t(row[j]) * H, v + u * step);
         }
-        if (w) {
-          float o[V];
+      }
 #pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = wj[j] * f[i];
-          store_vec(rows + size_t(row[j]) * H, v, Pack<T, V>::of(o));
-        } else {
-          store_vec(rows + size_t(row[j]) * H, v, av);
+      for (int u = 0; u < U; ++u) {
+        if (v + u * step >= nv) break;
+        float f[V];
+        av[u].unpack(f);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (row[j] < 0) continue;
+          if (DOT) {
+            float g[V];
+            bv[u][j].unpack(g);
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot[j] = fmaf(f[i], g[i], dot[j]);
+          }
+          if (w) {
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = wj[j] * f[i];
+            store_vec(rows + size_t(row[j]) * H, v + u * step, Pack<T, V>::of(o));
+          } else {
+            store_vec(rows + size_t(row[j]) * H, v + u * step, av[u]);
+          }
         }
       }
     }
     if (DOT) {
-      const float s = block_sums<kSlots>(dot, red);
+      const float s = block_sums<KB>(dot, red);
       const int j = j0 + int(threadIdx.x);
-      if (threadIdx.x < kSlots && j < k) dw[size_t(t) * k + j] = s;
+      if (threadIdx.x < KB && j < k) dw[size_t(t) * k + j] = s;
       __syncthreads();
     }
   }
 }
 
-// KB: slots unrolled (k <= KB).
 template <typename T, int V, bool DOT, int KB>
-__global__ void __launch_bounds__(kRowThreads, DOT && KB == kSlots ? 3 : 0) k_gather(const T* __restrict__ rows, const T* x, const float* __restrict__ w,
-                                                        const int32_t* __restrict__ p2r, int H, int k, T* out,
-                                                        float* __restrict__ dw) {
+__global__ void __launch_bounds__(kRowThreads, DOT && KB <= kSlots ? 3 : 0)
+    k_gather(const T* __restrict__ rows, const T* x, const float* __restrict__ w, const int32_t* __restrict__ p2r, int H, int k,
+             T* out, float* __restrict__ dw) {
+  constexpr int U = vectors_of(V, KB, DOT), SB = KB < kSlots ? KB : kSlots;  // slots in flight
   __shared__ float red[KB * 8];
   __shared__ int srow[KB];
   __shared__ float sw[KB];
@@ -118,40 +134,55 @@ __global__ void __launch_bounds__(kRowThreads, DOT && KB == kSlots ? 3 : 0) k_ga
 #pragma unroll
   for (int j = 0; j < KB; ++j) dot[j] = 0.0f;
   const int step = DOT ? int(blockDim.x) : int(blockDim.x * gridDim.y);
-  for (int v = DOT ? int(threadIdx.x) : int(blockIdx.y * blockDim.x + threadIdx.x); v < nv; v += step) {
-    float acc[V], xf[V];
+  for (int v = DOT ? int(threadIdx.x) : int(blockIdx.y * blockDim.x + threadIdx.x); v < nv; v += U * step) {
+    float acc[U][V];
+    Pack<T, V> xv[U];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = xf[i] = 0.0f;
-    Pack<T, V> xv;
-    if (x) xv = load_vec<T, V>(x + size_t(t) * H, v);
-    if (DOT) xv.unpack(xf);
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-    for (int j0 = 0; j0 < KB; j0 += kSlots) {
+      for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
+      if (x && v + u * step < nv) xv[u] = load_vec<T, V>(x + size_t(t) * H, v + u * step);
+    }
+#pragma unroll
+    for (int j0 = 0; j0 < KB; j0 += SB) {
       if (j0 >= k) break;
-      Pack<T, V> r[kSlots];
+      Pack<T, V> r[U][SB];
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j)
-        if (srow[j0 + j] >= 0) r[j] = load_vec_once<T, V>(rows + size_t(srow[j0 + j]) * H, v);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        if (srow[j0 + j] < 0) continue;
-        float f[V];
-        r[j].unpack(f);
-        const float wj = sw[j0 + j];
+        for (int j = 0; j < SB; ++j)
+          if (srow[j0 + j] >= 0 && v + u * step < nv) r[u][j] = load_vec_once<T, V>(rows + size_t(srow[j0 + j]) * H, v + u * step);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
-        if (DOT) {
+      for (int u = 0; u < U; ++u) {
+        if (v + u * step >= nv) break;
+        float xf[V];
+        if (DOT) xv[u].unpack(xf);
 #pragma unroll
-          for (int i = 0; i < V; ++i) dot[j0 + j] = fmaf(xf[i], f[i], dot[j0 + j]);
+        for (int j = 0; j < SB; ++j) {
+          if (srow[j0 + j] < 0) continue;
+          float f[V];
+          r[u][j].unpack(f);
+          const float wj = sw[j0 + j];
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[u][i] = fmaf(wj, f[i], acc[u][i]);
+          if (DOT) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot[j0 + j] = fmaf(xf[i], f[i], dot[j0 + j]);
+          }
         }
       }
     }
-    if (!DOT && x) {  // the residual, added last
-      xv.unpack(xf);
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += xf[i];
+    for (int u = 0; u < U; ++u) {
+      if (v + u * step >= nv) break;
+      if (!DOT && x) {  // the residual, added last
+        float xf[V];
+        xv[u].unpack(xf);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] += xf[i];
+      }
+      store_vec(out + size_t(t) * H, v + u * step, Pack<T, V>::of(acc[u]));
     }
-    store_vec(out + size_t(t) * H, v, Pack<T, V>::of(acc));
   }
   if (DOT) {
     const float s = block_sums<KB>(dot, red);
@@ -347,31 +378,37 @@ int row_threads(int nv) {  // as many threads as the row has vectors, at most kR
   return t < kRowThreads ? t : kRowThreads;
 }
 
-template <typename T, int V>
-cudaError_t spread(const RowArgs& g, cudaStream_t st) {
-  const int nv = g.H / V, threads = row_threads(nv);
-  const T *a = static_cast<const T*>(g.a), *b = static_cast<const T*>(g.b);
-  T* out = static_cast<T*>(g.out);
-  if (g.dw) {
-    k_spread<T, V, true><<<unsigned(g.T), threads, 0, st>>>(a, b, g.w, g.p2r, g.H, g.k, out, g.dw);
-  } else {
-    const dim3 grid(unsigned(g.T), unsigned((nv + threads - 1) / threads));
-    k_spread<T, V, false><<<grid, threads, 0, st>>>(a, nullptr, g.w, g.p2r, g.H, g.k, out, nullptr);
-  }
+template <typename T, int V, bool DOT, int KB>
+cudaError_t spread_of(const RowArgs& g, cudaStream_t st) {
+  const int nv = (g.H / V + vectors_of(V, KB, DOT) - 1) / vectors_of(V, KB, DOT), threads = row_threads(nv);
+  const dim3 grid(unsigned(g.T), DOT ? 1u : unsigned((nv + threads - 1) / threads));
+  k_spread<T, V, DOT, KB><<<grid, threads, 0, st>>>(static_cast<const T*>(g.a), static_cast<const T*>(g.b), g.w, g.p2r, g.H, g.k,
+                                                    static_cast<T*>(g.out), g.dw);
+  return cudaGetLastError();
+}
+
+template <typename T, int V, bool DOT, int KB>
+cudaError_t gather_of(const RowArgs& g, cudaStream_t st) {
+  const int nv = (g.H / V + vectors_of(V, KB, DOT) - 1) / vectors_of(V, KB, DOT), threads = row_threads(nv);
+  const dim3 grid(unsigned(g.T), DOT ? 1u : unsigned((nv + threads - 1) / threads));
+  k_gather<T, V, DOT, KB><<<grid, threads, 0, st>>>(static_cast<const T*>(g.a), static_cast<const T*>(g.b), g.w, g.p2r, g.H, g.k,
+                                                    static_cast<T*>(g.out), g.dw);
   return cudaGetLastError();
 }
 
 template <typename T, int V, bool DOT>
-cudaError_t gather_of(const RowArgs& g, cudaStream_t st) {
-  const int nv = g.H / V, threads = row_threads(nv);
-  const T *a = static_cast<const T*>(g.a), *b = static_cast<const T*>(g.b);
-  T* out = static_cast<T*>(g.out);
-  const dim3 grid(unsigned(g.T), DOT ? 1u : unsigned((nv + threads - 1) / threads));
-  if (g.k <= kSlots)
-    k_gather<T, V, DOT, kSlots><<<grid, threads, 0, st>>>(a, b, g.w, g.p2r, g.H, g.k, out, g.dw);
-  else
-    k_gather<T, V, DOT, MOE_MAX_TOPK><<<grid, threads, 0, st>>>(a, b, g.w, g.p2r, g.H, g.k, out, g.dw);
-  return cudaGetLastError();
+cudaError_t spread(const RowArgs& g, cudaStream_t st) {
+  return g.k <= 2   ? spread_of<T, V, DOT, 2>(g, st)
+         : g.k <= 4 ? spread_of<T, V, DOT, 4>(g, st)
+                    : spread_of<T, V, DOT, kSlots>(g, st);
+}
+
+template <typename T, int V, bool DOT>
+cudaError_t gather(const RowArgs& g, cudaStream_t st) {
+  return g.k <= 2        ? gather_of<T, V, DOT, 2>(g, st)
+         : g.k <= 4      ? gather_of<T, V, DOT, 4>(g, st)
+         : g.k <= kSlots ? gather_of<T, V, DOT, kSlots>(g, st)
+                         : gather_of<T, V, DOT, MOE_MAX_TOPK>(g, st);
 }
 
 template <typename T>
@@ -379,9 +416,10 @@ cudaError_t rows_of(const RowArgs& g, bool is_spread, cudaStream_t st) {
   constexpr int V = vec_width<T>();
   // 128-bit accesses where every row starts on 16 bytes; else one element at a time
   const bool wide = g.H % V == 0 && vec_aligned(g.a) && vec_aligned(g.b) && vec_aligned(g.out);
-  if (is_spread) return wide ? spread<T, V>(g, st) : spread<T, 1>(g, st);
-  if (g.dw) return wide ? gather_of<T, V, true>(g, st) : gather_of<T, 1, true>(g, st);
-  return wide ? gather_of<T, V, false>(g, st) : gather_of<T, 1, false>(g, st);
+  if (is_spread && g.dw) return wide ? spread<T, V, true>(g, st) : spread<T, 1, true>(g, st);
+  if (is_spread) return wide ? spread<T, V, false>(g, st) : spread<T, 1, false>(g, st);
+  if (g.dw) return wide ? gather<T, V, true>(g, st) : gather<T, 1, true>(g, st);
+  return wide ? gather<T, V, false>(g, st) : gather<T, 1, false>(g, st);
 }
 
 cudaError_t rows_any(const RowArgs& g, moe_dtype_t dt, bool is_spread, cudaStream_t st) {

@@ -84,7 +84,10 @@ def test_permutation_without_drops_equals_moe_permute(moe, cuda_device):
 SHAPES = [  # T, H, E, k, capacity, first id, end of ids
     (1, 2048, 8, 1, 0, 0, 8), (3, 1, 4, 2, 0, 0, 4), (16, 2048, 64, 8, 0, 0, 64), (5, 37, 6, 3, 2, -2, 8),
     (9, 257, 40, 32, 0, 0, 40), (40, 264, 12, 9, 10, -3, 12), (2, 7168, 256, 8, 0, 0, 256), (6, 64, 4, 2, 0, 5, 9),
-    (31, 4104, 16, 4, 3, 0, 16)]
+    (31, 4104, 16, 4, 3, 0, 16),
+    # several vectors or single elements to a thread, and several rounds of them
+    (5, 2047, 8, 4, 0, 0, 8), (4, 9001, 4, 2, 0, 0, 4), (3, 16400, 4, 1, 0, 0, 4), (6, 8200, 6, 3, 0, -1, 6), (3, 8191, 16, 8, 0, -4, 16),
+    (7, 5000, 9, 6, 0, 0, 9), (9, 1024, 4, 2, 3, 0, 4), (4, 4099, 20, 13, 0, 0, 20)]
 
 
 @pytest.mark.parametrize("T,H,E,k,cap,lo,hi", SHAPES)
