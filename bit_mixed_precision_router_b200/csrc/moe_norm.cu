@@ -338,6 +338,8 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
     zc = r * r * (s[1] * inv_h);
   };
   // One barrier per row: the second sum of row t and the first sums of the CTA's next row are joined together.
+  // the kernel that joins the partial sums may be launched; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int stage = 0, ahead = 1;
   // the gate of the next row, read a row ahead: reading it in its own row cost a fifth of the time (97 against 76 us)
   float gate = a.gate_tok ? a.gate_tok[blockIdx.x] : 1.0f;
@@ -463,13 +465,15 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
   }
 }
 
-// out[c] = sum over g of part[g][which][c], 32 columns per CTA, 32 row groups joined in shared memory
+// out[c] = sum over g of part[g][which][c], 32 columns per CTA, 32 row groups joined in shared memory.  Launched while the
+// kernel that writes `part` still runs (512 x 2048: 11.1 -> 10.4 us for both), so it waits for that one to be complete first.
 __global__ void __launch_bounds__(1024) k_norm_weight_sum(const float* __restrict__ part, int G, int H,
                                                           float* __restrict__ dw_post, float* __restrict__ dw_next) {
   __shared__ float s[32][33];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), g0 = threadIdx.x >> 5;
   float* out = blockIdx.y == 0 ? dw_post : dw_next;
   if (!out) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float v = 0.0f;
   if (c < H)
 #pragma unroll 8
@@ -650,8 +654,16 @@ cudaError_t launch_block_norm_bwd(const moe_block_norm_t& b, const void* z, cons
   int grid = 0;
   cudaError_t err = norm_any(a, dt, &grid, st);
   if (err != cudaSuccess || (!g.dw_post && !g.dw_next)) return err;
-  k_norm_weight_sum<<<dim3(unsigned((H + 31) / 32), 2), 1024, 0, st>>>(a.part, grid, H, g.dw_post, g.dw_next);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((H + 31) / 32), 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_norm_weight_sum, static_cast<const float*>(a.part), grid, H, g.dw_post, g.dw_next);
 }
 
 }  // namespace moe

@@ -462,9 +462,9 @@ typedef enum {
  * Requires K % 128 == 0, 1 <= N <= 2^30, K <= 2^20, N even with SwiGLU, ldx >= K and
  * ldx % 8 == 0, ldy >= M, ldr = 0 or >= M; x, w, scale 16-byte aligned, y and residual aligned to their
  * element; y overlaps no other input.  Any T from 0 to 2^22 - 64; the weights are read once per 64
- * tokens: made for decode batches (larger batches of whole experts are moe_grouped_ffn's, which takes
- * E = 1).  The first call on a device sets kernel attributes: make one call per shape to be
- * captured before a stream capture. */
+ * tokens (of small matrices per 16): made for decode batches (larger batches of whole experts are
+ * moe_grouped_ffn's, which takes E = 1).  The first call on a device sets kernel attributes: make one call per
+ * shape to be captured before a stream capture. */
 moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, const moe_linear_t* w, int64_t T, int64_t N,
                            int64_t K, moe_act_t act, const void* residual, int64_t ldr, void* y, int64_t ldy,
                            moe_dtype_t y_dtype, moe_stream_t stream);
