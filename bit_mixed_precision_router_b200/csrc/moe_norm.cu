@@ -4,7 +4,7 @@
 //   n = y rsqrt(mean y^2 + eps) w_post        (n = y without w_post)
 //   z = x + alpha a n,   h = z rsqrt(mean z^2 + eps) w_next
 // One CTA holds one row in registers, so each input is read once and z, h written once; the row
-// sums (two at most, dependent) are CTA reductions in fp32.  Bound by HBM (4096 x 7168 bf16: 48 us, 36 us at the copy's rate);
+// sums (two at most, dependent) are CTA reductions in fp32.  Bound by HBM (4096 x 7168 bf16: 46 us, 36 us at the copy's rate);
 // with an elementwise gate by half by its sigmoids.
 // Backward, from z, y and the gate (the statistics are recomputed from the row, which is read
 // anyway; nothing is saved by the forward pass), with r = rsqrt(mean z^2 + eps), q = rsqrt(mean y^2 + eps):
@@ -515,6 +515,10 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
   // several CTAs share an SM and one's loads run during the others' sums.
   if (nv <= 1024 && (a.T < 2 * kSms || nv <= 64))
     k_block_norm<T, V, 1, 1024, 1, ROUTED><<<rows, round32(nv), 0, st>>>(a);
+  else if (nv <= 1024 && nv > 768 && !ROUTED)
+    // up to 384 threads three CTAs of 55 registers fit an SM by themselves; beyond, 40 registers make room for the third (4096 x
+    // 7168 50 -> 46 us; at 1000 x 4096 it would cost 7.1 -> 8.5 us)
+    k_block_norm<T, V, 2, 512, ROUTED ? 2 : 3, ROUTED><<<rows, round32((nv + 1) / 2), 0, st>>>(a);
   else if (nv <= 1024)
     k_block_norm<T, V, 2, 512, 2, ROUTED><<<rows, round32((nv + 1) / 2), 0, st>>>(a);
   else if (nv <= 4096)
