@@ -456,7 +456,7 @@ typedef enum {
 
 /* y[t][n] = act(sum_k x[t][k] w[n][k]) + residual[t][n], for t < T and n < M (M = N, or N/2 with
  * SwiGLU).  No weight is rounded (W4: the group's fp32 sum is scaled; NVFP4: code times block scale is
- * exact in 16 bits), sums in fp32 in an order fixed by T, N and K, one rounding at the end.
+ * exact in 16 bits), sums in fp32 in an order fixed by T, N, K and the format, one rounding at the end.
  *   x bf16 or fp16, row t at x + t * ldx;  residual (NULL: none) and y of y_dtype, rows ldr and ldy
  *   elements apart; ldr = 0: one row for all tokens (a bias).  y may be residual (with ldy = ldr).
  * Requires K % 128 == 0, 1 <= N <= 2^30, K <= 2^20, N even with SwiGLU, ldx >= K and
@@ -584,7 +584,7 @@ size_t moe_block_norm_bwd_workspace_bytes(int64_t T, int64_t H);
  *   d = dz + r (w_next dh) - z r^3 <z, w_next dh> / H,  r = rsqrt(mean(z^2) + eps)      = dx
  *   dn = alpha a d,  dy = q (w_post dn) - y q^3 <y, w_post dn> / H,  q = rsqrt(mean(y^2) + eps)
  *   dgate = alpha a' d n (summed over the token's row for a gate per token)
- *   dw_post = sum_t dn y q,  dw_next = sum_t dh z r      (fp32, in an order fixed by T, H and the types)
+ *   dw_post = sum_t dn y q,  dw_next = sum_t dh z r      (fp32, in an order fixed by shapes, types and alignments)
  * z may be NULL if dh is.  Outputs must not overlap inputs, except that dx may be dz.  A gradient that
  * the step does not have (dy without y, dgate without gate, dw_post without w_post, dw_next without dh)
  * must be NULL.  Workspace: at least moe_block_norm_bwd_workspace_bytes(T, H), 16-byte aligned, contents
