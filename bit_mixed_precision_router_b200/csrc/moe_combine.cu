@@ -13,10 +13,10 @@ __global__ void k_combine(const uint16_t* __restrict__ y, const int32_t* __restr
   if (h >= H) return;
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int j = 0; j < k; ++j) {
-    const float wj = w[size_t(t) * k + j];
     const int row = p2r[size_t(t) * k + j];
-    if (row < 0) continue;  // a dropped pair (moe_permute_capacity)
-    const uint4 v = *reinterpret_cast<const uint4*>(y + size_t(row) * H + h);
+    const float wj = row < 0 ? 0.0f : w[size_t(t) * k + j];
+    // a dropped pair (moe_permute_capacity) adds nothing
+    const uint4 v = row < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(y + size_t(row) * H + h);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
