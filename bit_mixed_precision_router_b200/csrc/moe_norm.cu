@@ -466,9 +466,9 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
 }
 
 // out[c] = sum over g of part[g][which][c], 32 columns per CTA, 32 row groups joined in shared memory.  Launched while the
-// kernel that writes `part` still runs (512 x 2048: 11.1 -> 10.4 us for both), so it waits for that one to be complete first.
-__global__ void __launch_bounds__(1024) k_norm_weight_sum(const float* __restrict__ part, int G, int H,
-                                                          float* __restrict__ dw_post, float* __restrict__ dw_next) {
+// kernel that writes `part` still runs (512 x 2048: 11.1 -> 10.4 us for both), so it waits for that one to be complete first,
+// and `part` is no const __restrict__: it changes during this kernel, and is read through L2 (__ldcg), behind the wait.
+__global__ void __launch_bounds__(1024) k_norm_weight_sum(const float* part, int G, int H, float* dw_post, float* dw_next) {
   __shared__ float s[32][33];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), g0 = threadIdx.x >> 5;
   float* out = blockIdx.y == 0 ? dw_post : dw_next;
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(1024) k_norm_weight_sum(const float* __restric
   float v = 0.0f;
   if (c < H)
 #pragma unroll 8
-    for (int g = g0; g < G; g += 32) v += part[(size_t(g) * 2 + blockIdx.y) * H + c];
+    for (int g = g0; g < G; g += 32) v += __ldcg(part + (size_t(g) * 2 + blockIdx.y) * H + c);
   s[g0][threadIdx.x & 31] = v;
   __syncthreads();
   v = warp_sum(s[threadIdx.x & 31][g0]);
