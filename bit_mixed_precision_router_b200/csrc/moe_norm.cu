@@ -41,35 +41,35 @@ struct NormArgs {
 
 constexpr int kNormSlots = 8;  // routed rows in flight per thread
 
-// exp(v) and 1 / v for a sigmoid.  __fdividef is within 2 units of the last place below 2^126 and gives 0 above.  Of an
-// elementwise gate of 16 bits the approximations do: exp is off by (2 + 1.2 |v|) 2^-24 relative, far below the result's half step,
-// and values below 2^-126 become 0; a third of the instructions (2048 x 7168 with such a gate: 32.5 -> 30.4 us).
-template <typename T>
-MOE_DEVICE float exp_of(float v) {
-  if constexpr (sizeof(T) == 4) return expf(v);
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * 1.4426950408889634f));
-  return e;
-}
-template <typename T>
-MOE_DEVICE float inverse_of(float v) {
-  if constexpr (sizeof(T) == 4) return __fdividef(1.0f, v);
+MOE_DEVICE float rcp_approx(float v) {  // within one unit of the last place; 0 for v > 2^126
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-template <typename T>
-MOE_DEVICE float sigmoid_of(float v) {
-  return inverse_of<T>(1.0f + exp_of<T>(-v));
-}
 
-// The sigmoid and its derivative without the cancellation of a (1 - a): with e = exp(-|v|) <= 1,
-// sigmoid(|v|) = 1 / (1 + e), sigmoid(-|v|) = e / (1 + e) and the derivative e / (1 + e)^2.
-template <typename T>
+// The sigmoid: with e = exp(-|v|) <= 1, sigmoid(|v|) = 1 / (1 + e) and sigmoid(-|v|) = e / (1 + e): nothing overflows, and it
+// keeps its last places down to where fp32 ends.  The gates that are fp32 themselves, and all gradients (w_post's is fp32 whatever
+// the gate is), take these two.
+MOE_DEVICE float sigmoid_of(float v) {
+  const float e = expf(-fabsf(v)), s = rcp_approx(1.0f + e);
+  return v >= 0.0f ? s : e * s;
+}
+// The sigmoid and its derivative e / (1 + e)^2, without the cancellation of a (1 - a).
 MOE_DEVICE void sigmoid_grad(const float v, float& a, float& da) {
-  const float e = exp_of<T>(-fabsf(v)), s = inverse_of<T>(1.0f + e);
+  const float e = expf(-fabsf(v)), s = rcp_approx(1.0f + e);
   a = v >= 0.0f ? s : e * s;
   da = e * s * s;
+}
+
+// The sigmoid of an elementwise gate on its way into z, which has the gate's type.  For 16 bits ex2.approx.ftz does: 2^-22 relative
+// by itself and 1.3 |v| 2^-24 by the rounded product v log2(e), together below 2^-17, where z's half step is 2^-8 (bf16) or
+// 2^-11 (fp16); a sigmoid below 2^-126 becomes 0.  A third of the instructions: 2048 x 7168 bf16 29.1 us, with expf 31.9.
+template <typename T>
+MOE_DEVICE float gate_of(float v) {
+  if constexpr (sizeof(T) == 4) return sigmoid_of(v);
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+  return rcp_approx(1.0f + e);
 }
 
 // W: vectors of V elements per thread.  The row's loads are all issued before the first sum.  ROUTED: y is the
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_block_norm(NormArgs a) {
       }
     }
     float scale = a.alpha;
-    if (a.gate_tok) scale *= a.sigmoid ? sigmoid_of<float>(gate) : gate;
+    if (a.gate_tok) scale *= a.sigmoid ? sigmoid_of(gate) : gate;
     if (a.w_post) {
       float s[1] = {0.0f};
 #pragma unroll
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_block_norm(NormArgs a) {
         float g[V];
         gp[i].unpack(g);
 #pragma unroll
-        for (int e = 0; e < V; ++e) m[e] *= a.sigmoid ? sigmoid_of<T>(g[e]) : g[e];
+        for (int e = 0; e < V; ++e) m[e] *= a.sigmoid ? gate_of<T>(g[e]) : g[e];
       }
       xp[i].unpack(xf);
 #pragma unroll
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
     float at = gate, dat = 1.0f;  // the token's gate and its derivative
     if (a.gate_tok) {
       if (t + gridDim.x < a.T) gate = a.gate_tok[t + gridDim.x];
-      if (a.sigmoid) sigmoid_grad<float>(at, at, dat);
+      if (a.sigmoid) sigmoid_grad(at, at, dat);
     }
     float d[W][V];
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // [3]: <y, w_post d> (with the elementwise gate: <y, w_post a d>)
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           float c = g[e], dc = 1.0f;
-          if (a.sigmoid) sigmoid_grad<T>(g[e], c, dc);
+          if (a.sigmoid) sigmoid_grad(g[e], c, dc);
           dg[e] = a.alpha * dc * d[i][e] * (yf[e] * q * w[e]);
           d[i][e] *= c;
         }
