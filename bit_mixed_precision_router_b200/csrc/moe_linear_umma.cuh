@@ -123,7 +123,8 @@ MOE_DEVICE void w4_words_in_order(const uint4& q, uint32_t (&v)[16]) {
   }
 }
 // E2M1 codes times the block scales of their words 0..1 and 2..3.  bf16: the fp16 pattern shifted right by three has the
-// same exponent field under bf16's bias, the value times 2^-112, and the scale carries 2^112.
+// same exponent field under bf16's bias, the value times 2^-112, and the scale carries 2^104, so the product is the weight times
+// 2^-8, as in the mma.sync kernel: tokens overflow at the same sizes whatever their number.
 template <bool BF16>
 MOE_DEVICE void e2m1_words_in_order(const uint4& q, uint32_t scales, uint32_t (&v)[16]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -132,7 +133,7 @@ MOE_DEVICE void e2m1_words_in_order(const uint4& q, uint32_t scales, uint32_t (&
     const uint32_t h2 = e4m3_to_h2((scales >> (8 * (i >> 1))) & 0xFFu);
     uint32_t s2 = h2;
     if (BF16) {
-      s2 = float_to_bf16_bits(__half2float(__ushort_as_half(uint16_t(h2))) * 0x1p112f);
+      s2 = float_to_bf16_bits(__half2float(__ushort_as_half(uint16_t(h2))) * 0x1p104f);
       s2 |= s2 << 16;
     }
 #pragma unroll
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(Um<NTOK>::kThreads, Um<NTOK>::kCtas)
 #pragma unroll
     for (int i = 0; i < NTOK; ++i) o[i] += acc[i];
   }
-  finish_linear<1, 128, LD, 64>(a, red, part, t0, nt, W4 ? 1.0f : *a.gscale);
+  finish_linear<1, 128, LD, 64>(a, red, part, t0, nt, W4 ? 1.0f : *a.gscale * (BF16 ? 256.0f : 1.0f));
 }
 
 cudaError_t encode_tokens(CUtensorMap* map, const LinearArgs& a, bool bf16, int box_rows);

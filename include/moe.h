@@ -459,6 +459,9 @@ typedef enum {
  * exact in 16 bits), sums in fp32 in an order fixed by T, N, K and the format, one rounding at the end.
  *   x bf16 or fp16, row t at x + t * ldx;  residual (NULL: none) and y of y_dtype, rows ldr and ldy
  *   elements apart; ldr = 0: one row for all tokens (a bias).  y may be residual (with ldy = ldr).
+ * Range: the scales are applied to sums, W4's per group and NVFP4's per-tensor scale to the result, so bf16 tokens keep
+ * every partial sum finite for |x| < 2^118 (W4) and K |x| < 2^124 (NVFP4), whatever their number, where sum_k |x w| itself
+ * is finite; fp16 tokens always do.
  * Requires K % 128 == 0, 1 <= N <= 2^30, K <= 2^20, N even with SwiGLU, ldx >= K and
  * ldx % 8 == 0, ldy >= M, ldr = 0 or >= M; x, w, scale 16-byte aligned, y and residual aligned to their
  * element; y overlaps no other input.  Any T from 0 to 2^22 - 64; the weights are read once per 64
