@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
   auto statistics = [&](const float* s) {
     if (has_dh) r = rsqrtf(s[0] * inv_h + a.eps);
     if (has_post) q = rsqrtf(s[2] * inv_h + a.eps);
-    zc = r * r * (s[1] * inv_h);
+    zc = r * (r * (s[1] * inv_h));  // r * r alone overflows for eps below 2^-128
   };
   // One barrier per row: the second sum of row t and the first sums of the CTA's next row are joined together.
   // the kernel that joins the partial sums may be launched; it waits for this one's end
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS)) k_block_norm_bwd(N
     if (a.dgate_tok && threadIdx.x == 0) a.dgate_tok[t] = a.alpha * dat * q * s[3];
     if (has_y) {
       const float c = a.alpha * at;
-      const float yc = q * q * (s[3] * inv_h);  // dy = c q (w_post d - y yc)
+      const float yc = q * (q * (s[3] * inv_h));  // dy = c q (w_post d - y yc)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const int v = threadIdx.x + i * nth;
