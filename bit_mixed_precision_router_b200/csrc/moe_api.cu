@@ -70,6 +70,13 @@ moe_status_t check_route_shape(int64_t T, int64_t E, int64_t k) {
   return MOE_OK;
 }
 
+// check_route_shape without k <= E: with dropped pairs a token may choose experts of other ranks
+moe_status_t check_pairs_shape(int64_t T, int64_t E, int64_t k) {
+  if (T < 0) return MOE_ERR_INVALID_ARG;
+  if (E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || T > (1 << 30) / k) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -307,7 +314,7 @@ moe_status_t moe_grouped_ffn(const uint16_t* x, const moe_routing_t* routing, co
                              const uint8_t* bits, int64_t T, int64_t H, int64_t I, int64_t E, int64_t k,
                              uint16_t* y_rows, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   if (!experts) return MOE_ERR_INVALID_ARG;
-  moe_status_t s = check_route_shape(T, E, k);
+  moe_status_t s = check_pairs_shape(T, E, k);
   if (s != MOE_OK) return s;
   const moe_experts_t& ex = *experts;
   if (ex.fmt != MOE_FMT_W4G128 && ex.fmt != MOE_FMT_BITPLANE8 && ex.fmt != MOE_FMT_NVFP4)
@@ -435,13 +442,6 @@ moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, cons
     return MOE_ERR_MISALIGNED;
   return from_cuda(moe::launch_linear_w4(*w, x, ldx, x_dtype, int(T), int(N), int(K), act, residual, ldr, y, ldy, y_dtype,
                                          as_stream(stream)));
-}
-
-// check_route_shape without k <= E: with dropped pairs a token may choose experts of other ranks
-static moe_status_t check_pairs_shape(int64_t T, int64_t E, int64_t k) {
-  if (T < 0) return MOE_ERR_INVALID_ARG;
-  if (E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || T > (1 << 30) / k) return MOE_ERR_UNSUPPORTED_SHAPE;
-  return MOE_OK;
 }
 
 moe_status_t moe_permute_capacity(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t capacity,

@@ -366,7 +366,8 @@ size_t moe_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64
  * and compensation as above); expert e's weights are fetched to max_p bits[p].
  *   x bf16 [T][H];  routing: as written by moe_route_topk;  bits uint8 [T*k]
  *   (BITPLANE8 only, values 1..8, else may be NULL);  y_rows bf16 [T*k][H].
- * Requires H % 256 == 0, I % 128 == 0, the limits of moe_route_topk, and workspace
+ * Requires H % 256 == 0, I % 128 == 0, the limits of moe_route_topk (k may exceed E, as on a rank
+ * whose few experts are among those chosen: see moe_permute_capacity), and workspace
  * >= moe_ffn_workspace_bytes(...) (scratch: h, and for the GEMM path the token rows
  * gathered into routed order; contents need not be initialised).  Not bit-exact: fp32
  * accumulation order, the rounding of h (and, on the GEMM path, of each dequantised
@@ -493,7 +494,8 @@ moe_status_t moe_linear_w4(const void* x, int64_t ldx, moe_dtype_t x_dtype, cons
  * in sorted_pair, in ascending order (so sorted_pair stays a permutation).  topk_ids and topk_w are
  * not touched.  The routing serves moe_grouped_ffn (rows from expert_offsets[E] on are not
  * computed), the calls below and moe_combine (a dropped pair adds nothing); not
- * moe_grouped_ffn_w4a4, whose activation scale spans all T*k rows.
+ * moe_grouped_ffn_w4a4, whose activation scale spans all T*k rows, nor moe_expand_bits and
+ * moe_cache_step, which index by topk_ids and need each id in 0..E-1.
  *   ids int32 [T*k], 4-byte aligned; capacity >= 0 (0: no limit); 1 <= E <= MOE_MAX_EXPERTS,
  *   1 <= k <= MOE_MAX_TOPK (k may exceed E), T * k <= 2^30.  T = 0: nothing is written. */
 moe_status_t moe_permute_capacity(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t capacity,
