@@ -512,23 +512,26 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
   const int nv = a.H / V;
   const unsigned rows = unsigned(a.T);
   // Few rows: a vector per thread, the shortest path through the row.  Many: two vectors per thread, so that
-  // several CTAs share an SM and one's loads run during the others' sums.
-  if (nv <= 1024 && (a.T < 2 * kSms || nv <= 64))
+  // several CTAs share an SM and one's loads run during the others' sums.  Up to 384 threads three CTAs of 55 registers fit an SM by
+  // themselves; beyond, 40 registers make room for the third (4096 x 7168 50 -> 46 us; at 1000 x 4096 it would cost 7.1 -> 8.5 us).
+  // Routed rows keep two: their slots' indices and weights fill 64 registers as it is.
+  constexpr int wide_ctas = ROUTED ? 2 : 3;
+  if (nv <= 1024 && (a.T < 2 * kSms || nv <= 64)) {
     k_block_norm<T, V, 1, 1024, 1, ROUTED><<<rows, round32(nv), 0, st>>>(a);
-  else if (nv <= 1024 && nv > 768 && !ROUTED)
-    // up to 384 threads three CTAs of 55 registers fit an SM by themselves; beyond, 40 registers make room for the third (4096 x
-    // 7168 50 -> 46 us; at 1000 x 4096 it would cost 7.1 -> 8.5 us)
-    k_block_norm<T, V, 2, 512, ROUTED ? 2 : 3, ROUTED><<<rows, round32((nv + 1) / 2), 0, st>>>(a);
-  else if (nv <= 1024)
+  } else if (nv <= 768) {
     k_block_norm<T, V, 2, 512, 2, ROUTED><<<rows, round32((nv + 1) / 2), 0, st>>>(a);
-  else if (nv <= 4096)
+  } else if (nv <= 1024) {
+    k_block_norm<T, V, 2, 512, wide_ctas, ROUTED><<<rows, round32((nv + 1) / 2), 0, st>>>(a);
+  } else if (nv <= 4096) {
     k_block_norm<T, V, 4, V == 8 ? 512 : 1024, 1, ROUTED><<<rows, round32((nv + 3) / 4), 0, st>>>(a);
-  else if (V == 1 && nv <= 8192)
-    k_block_norm<T, V, 8, 1024, 1, ROUTED><<<rows, round32((nv + 7) / 8), 0, st>>>(a);
-  else if constexpr (V == 1)
-    k_block_norm<T, V, 16, 1024, 1, ROUTED><<<rows, round32((nv + 15) / 16), 0, st>>>(a);
-  else
-    return cudaErrorInvalidValue;
+  } else if constexpr (V == 1) {
+    if (nv <= 8192)
+      k_block_norm<T, V, 8, 1024, 1, ROUTED><<<rows, round32((nv + 7) / 8), 0, st>>>(a);
+    else
+      k_block_norm<T, V, 16, 1024, 1, ROUTED><<<rows, round32((nv + 15) / 16), 0, st>>>(a);
+  } else {
+    return cudaErrorInvalidValue;  // H <= 16384: at most 4096 vectors
+  }
   return cudaGetLastError();
 }
 
