@@ -198,8 +198,8 @@ struct Lin {
   static constexpr int kCI = kCG / KW;                        // of them each warp's
   static constexpr int kTokStride = kCG * 256 + 64;           // bytes per staged token; 64: no bank conflicts
   static constexpr int kTokBytes = 8 * NT * kTokStride;
-  // groups of weights in flight per warp; every one more is taken from L1, which holds the scales' lines (50304 x 7168,
-  // 1 token: two 44, four 49 us before the scales were read as vectors)
+  // groups of weights in flight per warp; with three CTAs per SM every one more is taken from L1, which holds the scales' lines
+  // (50304 x 7168, 1 token: two 44, four 49 us before the scales were read as vectors); launches of one CTA per SM have the same
   static constexpr int kDepth = NT == 1 ? 2 : 4;
   static constexpr int kRing = kDepth * 1024;                 // bytes per warp
   static constexpr int kSmem = 2 * kTokBytes + kWarps * kRing;

@@ -9,10 +9,12 @@
 //               registers: as in the mma.sync kernel no weight is rounded, and the tensor core only ever adds up one group;
 //   warp 8      one thread loads the tokens of each group by TMA (two boxes of 64 k, 128-byte swizzle) into a ring;
 //   warp 9      one thread issues eight tcgen05.mma (A from tensor memory, B from shared memory) per group.
-// Bound by the MMAs: with A from tensor memory one takes about 100 cycles however few its tokens (0.43 us per group and SM with
-// two CTAs, 0.72 with one CTA of 4 to 6 sets, so two CTAs of two sets share an SM; issuing the MMAs of several sets in turn,
-// dequantising ahead of them or a deeper token ring changed nothing or lost).  mma.sync has no such step but reads every
-// token from shared memory per 16 rows: 125 against 87 us with 32 tokens and 233 against 125 us with 64 (50304 x 7168).
+// An MMA with A from tensor memory takes about 100 cycles however few its tokens, eight a group; with one operand and one
+// accumulator per set a group's store, MMAs, load and additions follow one another (0.43 us per group and SM with two CTAs of two
+// sets, 0.72 with one CTA of 4 to 6; issuing the MMAs of several sets in turn, dequantising ahead of them or a deeper token ring
+// changed nothing or lost).  Half of the time at 50304 x 7168 and 64 tokens (125 us) would be MMAs alone if every SM had the same
+// share (62 us); the rest is that chain, and 393 blocks of rows on 296 resident CTAs, so that some CTAs take two.  mma.sync has no
+// such chain but reads every token from shared memory per 16 rows: 125 against 87 us with 32 tokens and 233 against 125 us with 64.
 // The sets' sums, and those of the cluster's CTAs on other parts of K, are joined in shared memory in a fixed order.
 // Every wait is bounded (mbar_wait): one that runs out sets the device error word and its role stops; the CTA still frees its
 // tensor memory.

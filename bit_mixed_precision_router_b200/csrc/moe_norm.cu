@@ -11,10 +11,12 @@
 //   d = dz + r (w_next dh) - z r^3 <z, w_next dh> / H                       (the gradient of x)
 //   dn = alpha a d;  dy = q (w_post dn) - y q^3 <y, w_post dn> / H;  dgate = alpha a' d n
 //   dw_next = sum_t dh z r,  dw_post = sum_t dn y q
-// 4096 x 7168 bf16, gate per token: 76 us, 54 us at the copy's rate.
+// 4096 x 7168 bf16, gate per token: 76 us, 54 us at the copy's rate; with an elementwise gate 122 us, 72 at the copy's rate.
 // A persistent grid: each CTA walks rows t = b, b + gridDim.x, ... with its columns fixed per
-// thread, so the weight gradients accumulate in registers (fp32) and each CTA writes one partial row;
-// a second kernel adds the partial rows in CTA order (no atomics: the result does not depend on timing).
+// thread, so the weight gradients accumulate in registers and each CTA writes one partial row; a second kernel adds the
+// partial rows in CTA order (no atomics: the result does not depend on timing).  These sums are fp32, T / CTAs terms in a CTA
+// and then the CTAs' (64 bits would take twice the registers, which bound the kernel): off by at most (T + 128) 2^-24 of the
+// terms' magnitudes.
 #include <atomic>
 #include <climits>
 #include <type_traits>

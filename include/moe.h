@@ -591,7 +591,8 @@ size_t moe_block_norm_bwd_workspace_bytes(int64_t T, int64_t H);
  *   d = dz + r (w_next dh) - z r^3 <z, w_next dh> / H,  r = rsqrt(mean(z^2) + eps)      = dx
  *   dn = alpha a d,  dy = q (w_post dn) - y q^3 <y, w_post dn> / H,  q = rsqrt(mean(y^2) + eps)
  *   dgate = alpha a' d n (summed over the token's row for a gate per token)
- *   dw_post = sum_t dn y q,  dw_next = sum_t dh z r      (fp32, in an order fixed by shapes, types and alignments)
+ *   dw_post = sum_t dn y q,  dw_next = sum_t dh z r      (fp32 sums, in an order fixed by shapes, types and alignments,
+ *                                                         off by at most (T + 128) 2^-24 of the terms' magnitudes)
  * z may be NULL if dh is.  Outputs must not overlap inputs, except that dx may be dz.  A gradient that
  * the step does not have (dy without y, dgate without gate, dw_post without w_post, dw_next without dh)
  * must be NULL.  Workspace: at least moe_block_norm_bwd_workspace_bytes(T, H), 16-byte aligned, contents
