@@ -570,7 +570,7 @@ typedef struct {
  * for the calls above); gate per token, pair_to_row and topk_w: 4 bytes.  |y|, |z| < 2^56 keep the
  * sums of squares finite, and alpha a rsqrt(mean(y^2) + eps) w_post, formed before it meets y, has to be finite.  The sigmoid
  * of a 16-bit elementwise gate v is off by at most (16 + 1.3 |v|) 2^-24 relative and 0 below 2^-126 on its way into the 16-bit z;
- * elsewhere, the gradients among it, a sigmoid is off by at most 16 2^-24.  Deterministic. */
+ * elsewhere, the gradients among it, a sigmoid is off by at most 16 2^-24 (below 2^-126 by 2^-148).  Deterministic. */
 moe_status_t moe_block_norm(const moe_block_norm_t* step, const void* x, moe_dtype_t dtype, int64_t T, int64_t H, void* z,
                             void* h, moe_stream_t stream);
 
